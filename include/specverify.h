@@ -286,6 +286,111 @@ SV_API sv_status sv_kv_commit(const sv_attn_desc *desc, int32_t num_layers, cons
                               void *stream);
 
 /* ------------------------------------------------------------------------
+ * Append: rotate the new rows and write them to the paged cache
+ * ------------------------------------------------------------------------
+ * The step before the verify attention: sv_verify_attention takes q already
+ * rotated and a cache that already holds the new rows. This call rotates q and
+ * k by their positions, writes K and V to the cache and q to q_out, for the N
+ * rows of a verify step or for whole (ragged) prompts.
+ *   desc       as for sv_verify_attention; num_q_rows is the largest number of
+ *              new rows of a sequence, 1 .. 1048576
+ *   rope       how q and k are rotated (below)
+ *   rows       the new rows and where they are (below)
+ *   kv         the cache, written in place
+ *   block_table, ctx_lens   as for sv_verify_attention; ctx_lens includes the
+ *              new rows: row i of sequence b goes to cache position
+ *              ctx_lens[b] - n_b + i, n_b = new_lens[b] (N without new_lens)
+ *   q_out      bf16 [B][N][Hq][D], contiguous; NULL with rows.q NULL
+ *   status_flags int32 [B] or NULL
+ * Rotation: with t the row's position, R = rotary_dim, c_j = cos_sin[t][j] and
+ * s_j = cos_sin[t][R/2 + j], the pair (x1, x2) becomes
+ * (x1 c_j - x2 s_j, x2 c_j + x1 s_j), every product and sum rounded once to
+ * fp32 and the result once to the output's type. Pairs are (x_j, x_{j+R/2}) in
+ * the half layout and (x_2j, x_2j+1) in the interleaved one; entries from R on
+ * are copied. A scaling for long contexts is in the table: its frequencies,
+ * and a factor on its entries.
+ * A sequence is left untouched (its rows of q_out too) and flagged
+ * SV_FLAG_BAD_CONTEXT when n_b is outside [0, N] or ctx_len outside
+ * [n_b, max_blocks_per_seq*16]. A page of a sequence is skipped, with its rows
+ * of q_out, when one of its new rows' positions is outside [0, max_position)
+ * (SV_FLAG_BAD_CONTEXT; with R = 0 positions are not read) or its block id is
+ * outside the pool (SV_FLAG_BAD_BLOCK); the sequence's other pages are written.
+ * Rows i >= n_b are padding: neither read nor written.
+ * Two sequences must not append to the same page. q_out, status_flags and the
+ * cache must not overlap an input or one another. Limits: D a multiple of 8 up
+ * to 256, R a multiple of 16 up to D, B <= 65535; q, k, v, q_out, the pools and
+ * cos_sin 16-byte aligned, row strides multiples of 8.
+ */
+typedef struct {
+    int32_t rotary_dim;          /* R; 0 = no rotation */
+    int32_t interleaved;         /* 0: pairs (x_j, x_{j+R/2}); 1: pairs (x_2j, x_2j+1) */
+    int32_t max_position;        /* rows of cos_sin */
+    const float *cos_sin;        /* fp32 [max_position][R]: R/2 cosines, then R/2 sines; NULL with R = 0 */
+} sv_rope_desc;
+
+typedef struct {
+    const void *q;               /* bf16, row (b, i) at q + (b*N + i) * q_stride: [Hq][D]; or NULL */
+    const void *k, *v;           /* bf16, likewise with kv_stride: [Hkv][D] */
+    int64_t q_stride;            /* elements between rows of q, >= Hq*D */
+    int64_t kv_stride;           /* elements between rows of k and of v, >= Hkv*D */
+    const int32_t *positions;    /* [B][N] rotation positions, or NULL: the cache positions */
+    const int32_t *new_lens;     /* [B] rows each sequence appends, or NULL: N */
+} sv_new_rows;
+
+SV_API sv_status sv_kv_append(const sv_attn_desc *desc, const sv_rope_desc *rope, const sv_new_rows *rows,
+                              const sv_kv_layer *kv, const int32_t *block_table, const int32_t *ctx_lens,
+                              void *q_out, int32_t *status_flags, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The 8-bit KV cache
+ * ------------------------------------------------------------------------
+ * K and V in e4m3 (OCP 8-bit floating point, 448 the largest value), one fp32
+ * scale for each page of 16 tokens, KV head and K or V: half the bytes of the
+ * bf16 cache in HBM and in the verify attention's stream, which is what bounds
+ * it. An entry stands for e4m3 value * scale.
+ * The calls that write the cache keep each page under a power of two 2^e, e the
+ * smallest integer in [-100, 119] with max|x| <= 448 * 2^e over the page's rows
+ * (finite entries; -100 for zeros), and store x * 2^-e rounded to nearest even.
+ * Changing the page's power of two as rows come and go then moves its other
+ * entries without another rounding (short of e4m3's subnormals), and rejected
+ * drafts leave no trace: the scale only depends on the rows kept. Entries that
+ * are not finite are stored as NaN. The attention takes any scales in
+ * [2^-100, 2^100] (smaller ones, zero too, count as 2^-100), for instance from a
+ * calibration; a page that a call then writes to is brought to its power of two.
+ */
+typedef struct {
+    void *k_pool;                /* e4m3 [num_blocks][Hkv][16][D] */
+    void *v_pool;                /* e4m3 [num_blocks][Hkv][16][D] */
+    float *scales;               /* fp32 [num_blocks][Hkv][2]: of K, of V */
+} sv_kv_q8;
+
+/* sv_kv_append into the 8-bit cache: same arguments, rules and errors, D in
+ * {64, 128}. The rotated k and v are rounded once, from fp32 to e4m3. A page
+ * that already holds rows of the sequence is read and written back under its
+ * new scale; bytes behind the last row are left as they were. */
+SV_API sv_status sv_kv_append_q8(const sv_attn_desc *desc, const sv_rope_desc *rope, const sv_new_rows *rows,
+                                 const sv_kv_q8 *kv, const int32_t *block_table, const int32_t *ctx_lens,
+                                 void *q_out, int32_t *status_flags, void *stream);
+
+/* sv_verify_attention over the 8-bit cache: same arguments, masks, limits and
+ * flags (q and out bf16; the pools 16-byte aligned, scales 8-byte aligned).
+ * A page with a block id outside the pool reads as zeros. */
+SV_API size_t sv_verify_attention_q8_workspace_size(const sv_attn_desc *desc);
+
+SV_API sv_status sv_verify_attention_q8(const sv_attn_desc *desc, const void *q, const sv_kv_q8 *kv,
+                                        const int32_t *block_table, const int32_t *ctx_lens,
+                                        const uint64_t *draft_mask, void *out, void *workspace,
+                                        size_t workspace_bytes, int32_t *status_flags, void *stream);
+
+/* sv_kv_commit over the 8-bit cache: same arguments, rules and flags, D in
+ * {64, 128}. Pages that receive a row are written back under the scale of the
+ * rows they keep; where nothing moves nothing is written. */
+SV_API sv_status sv_kv_commit_q8(const sv_attn_desc *desc, int32_t num_layers, const sv_kv_q8 *layers,
+                                 const int32_t *block_table, const int32_t *ctx_lens, const int32_t *accept_len,
+                                 const int32_t *accept_path, int32_t *new_ctx_lens, int32_t *status_flags,
+                                 void *stream);
+
+/* ------------------------------------------------------------------------
  * Weight-free drafts from earlier responses
  * ------------------------------------------------------------------------
  * Chain drafts looked up in earlier rollouts' responses instead of drawn from

@@ -19,7 +19,9 @@ __all__ = [
     "sv_verify_attention_workspace_size", "sv_verify_attention", "sv_verify_attention_noalloc", "sv_accept",
     "sv_accept_workspace_size",
     "SvCascadeDesc", "make_cascade_desc", "sv_cascade_attention_workspace_size", "sv_cascade_verify_attention",
-    "sv_kv_commit", "make_kv_layers", "SdController", "SvCtlConfig", "SvHistoryDesc", "sv_history_draft",
+    "sv_kv_commit", "make_kv_layers", "SvRopeDesc", "SvNewRows", "SvKVQ8", "make_rope_desc", "make_new_rows",
+    "make_kv_q8", "sv_kv_append", "sv_kv_append_q8", "sv_verify_attention_q8_workspace_size",
+    "sv_verify_attention_q8", "sv_kv_commit_q8", "make_kv_q8_layers", "SdController", "SvCtlConfig", "SvHistoryDesc", "sv_history_draft",
     "sv_status_string", "sv_last_error", "sv_version", "library_path",
     "sv_testing_philox4x32_10", "sv_testing_verify_attention_stalled", "SV_FLAG_TIMEOUT",
     "SV_FLAG_NONFINITE", "SV_FLAG_BAD_CONTEXT", "SV_FLAG_BAD_TOKEN", "SV_FLAG_BAD_BLOCK",
@@ -66,6 +68,20 @@ class SvCascadeDesc(C.Structure):
 
 class SvKVLayer(C.Structure):
     _fields_ = [("k_pool", C.c_void_p), ("v_pool", C.c_void_p)]
+
+
+class SvRopeDesc(C.Structure):
+    _fields_ = [("rotary_dim", C.c_int32), ("interleaved", C.c_int32), ("max_position", C.c_int32),
+                ("cos_sin", C.c_void_p)]
+
+
+class SvNewRows(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p), ("q_stride", C.c_int64),
+                ("kv_stride", C.c_int64), ("positions", C.c_void_p), ("new_lens", C.c_void_p)]
+
+
+class SvKVQ8(C.Structure):
+    _fields_ = [("k_pool", C.c_void_p), ("v_pool", C.c_void_p), ("scales", C.c_void_p)]
 
 
 class SvCtlConfig(C.Structure):
@@ -129,6 +145,18 @@ def _load() -> C.CDLL:
     L.sv_accept.restype = C.c_int
     L.sv_kv_commit.argtypes = [C.POINTER(SvAttnDesc), i32, C.POINTER(SvKVLayer), P, P, P, P, P, P, P]
     L.sv_kv_commit.restype = C.c_int
+    L.sv_kv_append.argtypes = [C.POINTER(SvAttnDesc), C.POINTER(SvRopeDesc), C.POINTER(SvNewRows),
+                               C.POINTER(SvKVLayer), P, P, P, P, P]
+    L.sv_kv_append.restype = C.c_int
+    L.sv_kv_append_q8.argtypes = [C.POINTER(SvAttnDesc), C.POINTER(SvRopeDesc), C.POINTER(SvNewRows),
+                                  C.POINTER(SvKVQ8), P, P, P, P, P]
+    L.sv_kv_append_q8.restype = C.c_int
+    L.sv_verify_attention_q8_workspace_size.argtypes = [C.POINTER(SvAttnDesc)]
+    L.sv_verify_attention_q8_workspace_size.restype = sz
+    L.sv_verify_attention_q8.argtypes = [C.POINTER(SvAttnDesc), P, C.POINTER(SvKVQ8), P, P, P, P, P, sz, P, P]
+    L.sv_verify_attention_q8.restype = C.c_int
+    L.sv_kv_commit_q8.argtypes = [C.POINTER(SvAttnDesc), i32, C.POINTER(SvKVQ8), P, P, P, P, P, P, P]
+    L.sv_kv_commit_q8.restype = C.c_int
     L.sv_ctl_default_config.argtypes = [C.POINTER(SvCtlConfig)]
     L.sv_ctl_default_config.restype = None
     L.sv_ctl_create.argtypes = [C.POINTER(SvCtlConfig)]
@@ -287,6 +315,103 @@ def sv_kv_commit(desc: SvAttnDesc, layers, block_table, ctx_lens, accept_len, ac
 def make_kv_layers(layers) -> C.Array:
     """The SvKVLayer array of sv_kv_commit, built once for repeated calls."""
     return (SvKVLayer * len(layers))(*[SvKVLayer(_ptr(k), _ptr(v)) for k, v in layers])
+
+
+def make_rope_desc(cos_sin, interleaved: bool = False) -> SvRopeDesc:
+    """How sv_kv_append rotates: ``cos_sin`` fp32 [max_position][rotary_dim], half of a row cosines, then the
+    sines; None rotates nothing. The table is kept alive on the returned object."""
+    if cos_sin is None:
+        return SvRopeDesc(0, int(interleaved), 0, None)
+    if cos_sin.dim() != 2 or not cos_sin.is_contiguous() or str(cos_sin.dtype) != "torch.float32":
+        raise ValueError("cos_sin must be a contiguous fp32 [max_position][rotary_dim] tensor")
+    d = SvRopeDesc(cos_sin.shape[1], int(interleaved), cos_sin.shape[0], _ptr(cos_sin))
+    d._keep = cos_sin
+    return d
+
+
+def _row_stride(x, what: str) -> int:
+    """Elements between the rows of a bf16 [B][N][H][D] tensor whose heads lie side by side."""
+    if x.dim() != 4 or str(x.dtype) != "torch.bfloat16":
+        raise ValueError(f"{what} must be a bf16 [B][N][heads][D] tensor")
+    B, N, H, D = x.shape
+    if (D > 1 and x.stride(3) != 1) or (H > 1 and x.stride(2) != D):
+        raise ValueError(f"{what}: the heads of a row must lie side by side")
+    row = x.stride(1) if N > 1 else (x.stride(0) if B > 1 else H * D)
+    if B > 1 and N > 1 and x.stride(0) != N * row:
+        raise ValueError(f"{what}: the rows of all sequences must be evenly spaced")
+    return row
+
+
+def make_new_rows(q, k, v, positions=None, new_lens=None) -> SvNewRows:
+    """The new rows of sv_kv_append: q [B][N][Hq][D] (or None), k and v [B][N][Hkv][D] bf16, each possibly a slice
+    of a wider row (a fused projection's output); positions int32 [B][N], new_lens int32 [B] or None. The tensors
+    are kept alive on the returned object."""
+    ks, vs = _row_stride(k, "k"), _row_stride(v, "v")
+    if ks != vs or k.shape != v.shape:
+        raise ValueError("k and v must have the same shape and row stride")
+    if q is not None and (q.shape[:2] != k.shape[:2] or q.shape[3] != k.shape[3]):
+        raise ValueError("q, k and v must have the same sequences, rows and head size")
+    for x, shape, what in ((positions, k.shape[:2], "positions"), (new_lens, k.shape[:1], "new_lens")):
+        if x is not None and (x.shape != shape or not x.is_contiguous() or str(x.dtype) != "torch.int32"):
+            raise ValueError(f"{what} must be a contiguous int32 {list(shape)} tensor")
+    d = SvNewRows(_ptr(q), _ptr(k), _ptr(v), 0 if q is None else _row_stride(q, "q"), ks, _ptr(positions),
+                  _ptr(new_lens))
+    d._keep = (q, k, v, positions, new_lens)
+    return d
+
+
+def make_kv_q8(k_pool, v_pool, scales) -> SvKVQ8:
+    """One layer of the 8-bit cache: e4m3 pools [num_blocks][Hkv][16][D], fp32 scales [num_blocks][Hkv][2]
+    (tensors, kept alive on the returned object, or device addresses)."""
+    for x, name in ((k_pool, "torch.float8_e4m3fn"), (v_pool, "torch.float8_e4m3fn"), (scales, "torch.float32")):
+        if hasattr(x, "dtype") and (str(x.dtype) != name or not x.is_contiguous()):
+            raise ValueError(f"expected a contiguous {name} tensor, got {x.dtype}")
+    d = SvKVQ8(_ptr(k_pool), _ptr(v_pool), _ptr(scales))
+    d._keep = (k_pool, v_pool, scales)
+    return d
+
+
+def make_kv_q8_layers(layers) -> C.Array:
+    """The SvKVQ8 array of sv_kv_commit_q8, built once for repeated calls."""
+    each = [make_kv_q8(*x) for x in layers]
+    arr = (SvKVQ8 * len(each))(*each)
+    arr._keep = each
+    return arr
+
+
+def sv_kv_append(desc: SvAttnDesc, rope: SvRopeDesc, rows: SvNewRows, kv: SvKVLayer, block_table, ctx_lens, q_out,
+                 status_flags=None, stream=None) -> None:
+    """Rotate the new rows' q and k, write k and v to the paged bf16 cache and q to q_out."""
+    _check(_L().sv_kv_append(C.byref(desc), C.byref(rope), C.byref(rows), C.byref(kv), _ptr(block_table),
+                             _ptr(ctx_lens), _ptr(q_out), _ptr(status_flags), _stream(stream)))
+
+
+def sv_kv_append_q8(desc: SvAttnDesc, rope: SvRopeDesc, rows: SvNewRows, kv: SvKVQ8, block_table, ctx_lens, q_out,
+                    status_flags=None, stream=None) -> None:
+    """sv_kv_append into the 8-bit cache."""
+    _check(_L().sv_kv_append_q8(C.byref(desc), C.byref(rope), C.byref(rows), C.byref(kv), _ptr(block_table),
+                                _ptr(ctx_lens), _ptr(q_out), _ptr(status_flags), _stream(stream)))
+
+
+def sv_verify_attention_q8_workspace_size(desc: SvAttnDesc) -> int:
+    return int(_L().sv_verify_attention_q8_workspace_size(C.byref(desc)))
+
+
+def sv_verify_attention_q8(desc: SvAttnDesc, q, kv: SvKVQ8, block_table, ctx_lens, draft_mask, out, workspace,
+                           workspace_bytes: int, status_flags=None, stream=None) -> None:
+    """sv_verify_attention over the 8-bit cache."""
+    _check(_L().sv_verify_attention_q8(C.byref(desc), _ptr(q), C.byref(kv), _ptr(block_table), _ptr(ctx_lens),
+                                       _ptr(draft_mask), _ptr(out), _ptr(workspace), int(workspace_bytes),
+                                       _ptr(status_flags), _stream(stream)))
+
+
+def sv_kv_commit_q8(desc: SvAttnDesc, layers, block_table, ctx_lens, accept_len, accept_path, new_ctx_lens,
+                    status_flags=None, stream=None) -> None:
+    """sv_kv_commit over the 8-bit cache; layers: a sequence of (k_pool, v_pool, scales), or an array built once
+    with ``make_kv_q8_layers``."""
+    arr = layers if isinstance(layers, C.Array) else make_kv_q8_layers(layers)
+    _check(_L().sv_kv_commit_q8(C.byref(desc), len(layers), arr, _ptr(block_table), _ptr(ctx_lens), _ptr(accept_len),
+                                _ptr(accept_path), _ptr(new_ctx_lens), _ptr(status_flags), _stream(stream)))
 
 
 def sv_history_draft(desc: SvHistoryDesc, history_tokens, history_lens, history_reward, history_group,

@@ -6,6 +6,7 @@
 #include <string.h>
 
 #include "sv_internal.h"
+#include "sv_q8.h"
 
 namespace {
 
@@ -248,6 +249,149 @@ sv_status check_accept_desc(const sv_accept_desc *d, float temperature, sv::Acce
     return SV_OK;
 }
 
+// Checks of the append calls; fills p.
+sv_status check_append(const sv_attn_desc *d, const sv_rope_desc *rope, const sv_new_rows *rows, void *k_pool,
+                       void *v_pool, float *scales, bool q8, const int32_t *block_table, const int32_t *ctx_lens, void *q_out, int32_t *status_flags,
+                       sv::AppendParams *p) {
+    if (!d) return fail(SV_ERR_INVALID_ARG, "desc is NULL");
+    if (!rope || !rows) return fail(SV_ERR_INVALID_ARG, "rope or rows is NULL");
+    if (d->num_seqs < 0 || d->num_seqs > 65535) return fail(SV_ERR_INVALID_ARG, "num_seqs must be in [0, 65535]");
+    if (d->num_q_rows < 1 || d->num_q_rows > (1 << 20))
+        return fail(SV_ERR_INVALID_ARG, "num_q_rows must be in [1, 1048576]");
+    if (d->num_q_heads < 1 || d->num_kv_heads < 1 || d->num_q_heads > 65535 || d->num_kv_heads > 65535)
+        return fail(SV_ERR_INVALID_ARG, "num_q_heads and num_kv_heads must be in [1, 65535]");
+    if (q8 ? d->head_dim != 64 && d->head_dim != 128 : d->head_dim < 8 || d->head_dim > 256 || d->head_dim % 8)
+        return fail(SV_ERR_UNSUPPORTED, q8 ? "head_dim must be 64 or 128"
+                                           : "head_dim must be a multiple of 8 in [8, 256]");
+    if (d->block_size != sv::PAGE) return fail(SV_ERR_UNSUPPORTED, "block_size must be 16");
+    if (d->max_blocks_per_seq < 1) return fail(SV_ERR_INVALID_ARG, "max_blocks_per_seq < 1");
+    if (d->num_blocks < 1) return fail(SV_ERR_INVALID_ARG, "num_blocks < 1");
+    if ((long long)d->max_blocks_per_seq * sv::PAGE > (1LL << 30)) return fail(SV_ERR_UNSUPPORTED, "context too long");
+    if (rope->rotary_dim < 0 || rope->rotary_dim > d->head_dim || rope->rotary_dim % 16)
+        return fail(SV_ERR_UNSUPPORTED, "rotary_dim must be a multiple of 16 in [0, head_dim]");
+    if (rope->interleaved != 0 && rope->interleaved != 1)
+        return fail(SV_ERR_INVALID_ARG, "interleaved must be 0 or 1");
+    if (rope->rotary_dim > 0 && (rope->max_position < 1 || !rope->cos_sin || !aligned(rope->cos_sin, 16)))
+        return fail(SV_ERR_INVALID_ARG, "cos_sin must be a 16-byte aligned table of at least one position");
+    if (d->num_seqs == 0) return SV_OK;
+    if (!rows->k || !rows->v || !block_table || !ctx_lens) return fail(SV_ERR_INVALID_ARG, "a required pointer is NULL");
+    if (!rows->q != !q_out) return fail(SV_ERR_INVALID_ARG, "q and q_out go together");
+    if (!aligned(rows->k, 16) || !aligned(rows->v, 16) || (q_out && (!aligned(rows->q, 16) || !aligned(q_out, 16))))
+        return fail(SV_ERR_INVALID_ARG, "q, k, v and q_out must be 16-byte aligned");
+    const long long qw = (long long)d->num_q_heads * d->head_dim, kw = (long long)d->num_kv_heads * d->head_dim;
+    const long long most = 1LL << 40;
+    if (q_out && (rows->q_stride < qw || rows->q_stride % 8 || rows->q_stride > most))
+        return fail(SV_ERR_INVALID_ARG, "q_stride must be a multiple of 8 of at least num_q_heads * head_dim");
+    if (rows->kv_stride < kw || rows->kv_stride % 8 || rows->kv_stride > most)
+        return fail(SV_ERR_INVALID_ARG, "kv_stride must be a multiple of 8 of at least num_kv_heads * head_dim");
+    if (!aligned(block_table, 4) || !aligned(ctx_lens, 4) || (status_flags && !aligned(status_flags, 4)) ||
+        (rows->positions && !aligned(rows->positions, 4)) || (rows->new_lens && !aligned(rows->new_lens, 4)))
+        return fail(SV_ERR_INVALID_ARG, "misaligned table, length, position or status pointer");
+    if (!k_pool || !v_pool || !aligned(k_pool, 16) || !aligned(v_pool, 16))
+        return fail(SV_ERR_INVALID_ARG, "pool NULL or not 16-byte aligned");
+    if (q8 && (!scales || !aligned(scales, 8))) return fail(SV_ERR_INVALID_ARG, "scales NULL or not 8-byte aligned");
+    {
+        // CTAs write their outputs while others still read: no output over an input or another output
+        const size_t T = (size_t)d->num_seqs * d->num_q_rows, B4 = (size_t)d->num_seqs * 4;
+        const size_t heads = (size_t)d->num_blocks * d->num_kv_heads;
+        const size_t pool = heads * sv::PAGE * d->head_dim * (q8 ? 1 : 2);
+        const void *out[] = {q_out, status_flags, k_pool, v_pool, scales};
+        const size_t out_bytes[] = {T * (size_t)qw * 2, B4, pool, pool, heads * 8};
+        const void *in[] = {q_out ? rows->q : nullptr, rows->k, rows->v, block_table, ctx_lens, rows->positions,
+                            rows->new_lens, rope->rotary_dim > 0 ? rope->cos_sin : nullptr};
+        const size_t in_bytes[] = {((T - 1) * rows->q_stride + qw) * 2, ((T - 1) * rows->kv_stride + kw) * 2,
+                                   ((T - 1) * rows->kv_stride + kw) * 2, B4 * (size_t)d->max_blocks_per_seq, B4,
+                                   T * 4, B4, (size_t)rope->max_position * rope->rotary_dim * 4};
+        for (int o = 0; o < 5; ++o) {
+            for (int i = 0; i < 8; ++i)
+                if (overlaps(out[o], out_bytes[o], in[i], in_bytes[i]))
+                    return fail(SV_ERR_INVALID_ARG, "q_out, status_flags and the cache must not overlap an input");
+            for (int i = 0; i < o; ++i)
+                if (overlaps(out[o], out_bytes[o], out[i], out_bytes[i]))
+                    return fail(SV_ERR_INVALID_ARG, "q_out, status_flags and the cache must not overlap");
+        }
+    }
+    *p = sv::AppendParams{};
+    p->q = static_cast<const uint16_t *>(rows->q);
+    p->k = static_cast<const uint16_t *>(rows->k);
+    p->v = static_cast<const uint16_t *>(rows->v);
+    p->q_stride = rows->q_stride;
+    p->kv_stride = rows->kv_stride;
+    p->positions = rows->positions;
+    p->new_lens = rows->new_lens;
+    p->cos_sin = rope->cos_sin;
+    p->block_table = block_table;
+    p->ctx_lens = ctx_lens;
+    p->q_out = static_cast<uint16_t *>(q_out);
+    p->k_pool = k_pool;
+    p->v_pool = v_pool;
+    p->scales = scales;
+    p->status = status_flags;
+    p->B = d->num_seqs;
+    p->N = d->num_q_rows;
+    p->Hq = d->num_q_heads;
+    p->Hkv = d->num_kv_heads;
+    p->D = d->head_dim;
+    p->R = rope->rotary_dim;
+    p->interleaved = rope->interleaved;
+    p->max_position = rope->max_position;
+    p->max_blocks = d->max_blocks_per_seq;
+    p->num_blocks = d->num_blocks;
+    return SV_OK;
+}
+
+sv_status check_q8(const sv_kv_q8 *kv) {
+    if (!kv || !kv->k_pool || !kv->v_pool || !kv->scales) return fail(SV_ERR_INVALID_ARG, "a pool or scales is NULL");
+    if (!aligned(kv->k_pool, 16) || !aligned(kv->v_pool, 16) || !aligned(kv->scales, 8))
+        return fail(SV_ERR_INVALID_ARG, "the pools must be 16-byte aligned, scales 8-byte aligned");
+    return SV_OK;
+}
+
+// Checks of sv_kv_commit's arguments that both caches share, the layers apart.
+sv_status check_commit(const sv_attn_desc *d, int32_t num_layers, const void *layers, bool q8) {
+    if (!d) return fail(SV_ERR_INVALID_ARG, "desc is NULL");
+    if (d->num_seqs < 0) return fail(SV_ERR_INVALID_ARG, "num_seqs < 0");
+    if (d->num_q_rows < 1 || d->num_q_rows > 64) return fail(SV_ERR_INVALID_ARG, "num_q_rows must be in [1, 64]");
+    if (d->num_kv_heads < 1 || d->num_kv_heads > 65535) return fail(SV_ERR_INVALID_ARG, "num_kv_heads must be in [1, 65535]");
+    if (q8 ? d->head_dim != 64 && d->head_dim != 128 : d->head_dim < 8 || d->head_dim > 256 || d->head_dim % 8)
+        return fail(SV_ERR_UNSUPPORTED, q8 ? "head_dim must be 64 or 128"
+                                           : "head_dim must be a multiple of 8 in [8, 256]");
+    if (d->block_size != sv::PAGE) return fail(SV_ERR_UNSUPPORTED, "block_size must be 16");
+    if (d->max_blocks_per_seq < 1) return fail(SV_ERR_INVALID_ARG, "max_blocks_per_seq < 1");
+    if (d->num_blocks < 1) return fail(SV_ERR_INVALID_ARG, "num_blocks < 1");
+    if ((long long)d->max_blocks_per_seq * sv::PAGE > (1LL << 30)) return fail(SV_ERR_UNSUPPORTED, "context too long");
+    if (num_layers < 1 || num_layers > SV_COMMIT_MAX_LAYERS)
+        return fail(SV_ERR_INVALID_ARG, "num_layers must be in [1, %d]", SV_COMMIT_MAX_LAYERS);
+    if (!layers) return fail(SV_ERR_INVALID_ARG, "layers is NULL");
+    return SV_OK;
+}
+
+// The arrays of sv_kv_commit that both caches share.
+sv_status check_commit_arrays(const sv_attn_desc *d, const int32_t *block_table, const int32_t *ctx_lens,
+                              const int32_t *accept_len, const int32_t *accept_path, int32_t *new_ctx_lens,
+                              int32_t *status_flags) {
+    if (!block_table || !ctx_lens || !accept_len || !new_ctx_lens)
+        return fail(SV_ERR_INVALID_ARG, "a required pointer is NULL");
+    if (d->num_q_rows > 1 && !accept_path) return fail(SV_ERR_INVALID_ARG, "accept_path is NULL");
+    if (!aligned(block_table, 4) || !aligned(ctx_lens, 4) || !aligned(accept_len, 4) || !aligned(new_ctx_lens, 4) ||
+        (accept_path && !aligned(accept_path, 4)) || (status_flags && !aligned(status_flags, 4)))
+        return fail(SV_ERR_INVALID_ARG, "misaligned pointer");
+    // every CTA of a sequence reads its table row, length, accept length and
+    // path while one of them writes the new length and the status: the
+    // outputs must not alias any input (an in-place length update would let
+    // late CTAs read the new length)
+    const size_t B4 = (size_t)d->num_seqs * 4;
+    const void *in[] = {block_table, ctx_lens, accept_len, accept_path};
+    const size_t in_bytes[] = {B4 * (size_t)d->max_blocks_per_seq, B4, B4,
+                               B4 * (size_t)(d->num_q_rows > 1 ? d->num_q_rows - 1 : 1)};
+    for (int i = 0; i < 4; ++i)
+        if (overlaps(new_ctx_lens, B4, in[i], in_bytes[i]) || overlaps(status_flags, B4, in[i], in_bytes[i]))
+            return fail(SV_ERR_INVALID_ARG, "new_ctx_lens and status_flags must not overlap an input array");
+    if (overlaps(new_ctx_lens, B4, status_flags, B4))
+        return fail(SV_ERR_INVALID_ARG, "new_ctx_lens and status_flags overlap");
+    return SV_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -298,44 +442,14 @@ sv_status sv_accept(const sv_accept_desc *d, const float *target_logits, const f
 sv_status sv_kv_commit(const sv_attn_desc *d, int32_t num_layers, const sv_kv_layer *layers,
                        const int32_t *block_table, const int32_t *ctx_lens, const int32_t *accept_len,
                        const int32_t *accept_path, int32_t *new_ctx_lens, int32_t *status_flags, void *stream) {
-    if (!d) return fail(SV_ERR_INVALID_ARG, "desc is NULL");
-    if (d->num_seqs < 0) return fail(SV_ERR_INVALID_ARG, "num_seqs < 0");
-    if (d->num_q_rows < 1 || d->num_q_rows > 64) return fail(SV_ERR_INVALID_ARG, "num_q_rows must be in [1, 64]");
-    if (d->num_kv_heads < 1 || d->num_kv_heads > 65535) return fail(SV_ERR_INVALID_ARG, "num_kv_heads must be in [1, 65535]");
-    if (d->head_dim < 8 || d->head_dim > 256 || d->head_dim % 8)
-        return fail(SV_ERR_UNSUPPORTED, "head_dim must be a multiple of 8 in [8, 256]");
-    if (d->block_size != sv::PAGE) return fail(SV_ERR_UNSUPPORTED, "block_size must be 16");
-    if (d->max_blocks_per_seq < 1) return fail(SV_ERR_INVALID_ARG, "max_blocks_per_seq < 1");
-    if (d->num_blocks < 1) return fail(SV_ERR_INVALID_ARG, "num_blocks < 1");
-    if ((long long)d->max_blocks_per_seq * sv::PAGE > (1LL << 30)) return fail(SV_ERR_UNSUPPORTED, "context too long");
-    if (num_layers < 1 || num_layers > SV_COMMIT_MAX_LAYERS)
-        return fail(SV_ERR_INVALID_ARG, "num_layers must be in [1, %d]", SV_COMMIT_MAX_LAYERS);
-    if (!layers) return fail(SV_ERR_INVALID_ARG, "layers is NULL");
+    sv_status s = check_commit(d, num_layers, layers, false);
+    if (s != SV_OK) return s;
     for (int l = 0; l < num_layers; ++l)
         if (!layers[l].k_pool || !layers[l].v_pool || !aligned(layers[l].k_pool, 16) || !aligned(layers[l].v_pool, 16))
             return fail(SV_ERR_INVALID_ARG, "layer %d: pool NULL or not 16-byte aligned", l);
     if (d->num_seqs == 0) return SV_OK;
-    if (!block_table || !ctx_lens || !accept_len || !new_ctx_lens)
-        return fail(SV_ERR_INVALID_ARG, "a required pointer is NULL");
-    if (d->num_q_rows > 1 && !accept_path) return fail(SV_ERR_INVALID_ARG, "accept_path is NULL");
-    if (!aligned(block_table, 4) || !aligned(ctx_lens, 4) || !aligned(accept_len, 4) || !aligned(new_ctx_lens, 4) ||
-        (accept_path && !aligned(accept_path, 4)) || (status_flags && !aligned(status_flags, 4)))
-        return fail(SV_ERR_INVALID_ARG, "misaligned pointer");
-    {
-        // every CTA of a sequence reads its table row, length, accept length and
-        // path while one of them writes the new length and the status: the
-        // outputs must not alias any input (an in-place length update would let
-        // late CTAs read the new length)
-        const size_t B4 = (size_t)d->num_seqs * 4;
-        const void *in[] = {block_table, ctx_lens, accept_len, accept_path};
-        const size_t in_bytes[] = {B4 * (size_t)d->max_blocks_per_seq, B4, B4,
-                                   B4 * (size_t)(d->num_q_rows > 1 ? d->num_q_rows - 1 : 1)};
-        for (int i = 0; i < 4; ++i)
-            if (overlaps(new_ctx_lens, B4, in[i], in_bytes[i]) || overlaps(status_flags, B4, in[i], in_bytes[i]))
-                return fail(SV_ERR_INVALID_ARG, "new_ctx_lens and status_flags must not overlap an input array");
-        if (overlaps(new_ctx_lens, B4, status_flags, B4))
-            return fail(SV_ERR_INVALID_ARG, "new_ctx_lens and status_flags overlap");
-    }
+    if ((s = check_commit_arrays(d, block_table, ctx_lens, accept_len, accept_path, new_ctx_lens, status_flags)) != SV_OK)
+        return s;
     sv::CommitLaunch c;
     memset(&c, 0, sizeof c);
     c.block_table = block_table;
@@ -356,6 +470,92 @@ sv_status sv_kv_commit(const sv_attn_desc *d, int32_t num_layers, const sv_kv_la
         c.v[l] = static_cast<uint16_t *>(layers[l].v_pool);
     }
     cudaError_t e = sv::launch_kv_commit(c, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(SV_ERR_CUDA, "kv commit launch: %s", cudaGetErrorString(e));
+    return SV_OK;
+}
+
+sv_status sv_kv_append(const sv_attn_desc *d, const sv_rope_desc *rope, const sv_new_rows *rows,
+                       const sv_kv_layer *kv, const int32_t *block_table, const int32_t *ctx_lens, void *q_out,
+                       int32_t *status_flags, void *stream) {
+    sv::AppendParams p;
+    sv_status s = check_append(d, rope, rows, kv ? kv->k_pool : nullptr, kv ? kv->v_pool : nullptr, nullptr, false,
+                               block_table, ctx_lens, q_out, status_flags, &p);
+    if (s != SV_OK || d->num_seqs == 0) return s;
+    cudaError_t e = sv::launch_append(p, false, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(SV_ERR_CUDA, "append launch: %s", cudaGetErrorString(e));
+    return SV_OK;
+}
+
+sv_status sv_kv_append_q8(const sv_attn_desc *d, const sv_rope_desc *rope, const sv_new_rows *rows,
+                          const sv_kv_q8 *kv, const int32_t *block_table, const int32_t *ctx_lens, void *q_out,
+                          int32_t *status_flags, void *stream) {
+    sv::AppendParams p;
+    sv_status s = check_append(d, rope, rows, kv ? kv->k_pool : nullptr, kv ? kv->v_pool : nullptr,
+                               kv ? kv->scales : nullptr, true, block_table, ctx_lens, q_out, status_flags, &p);
+    if (s != SV_OK || d->num_seqs == 0) return s;
+    cudaError_t e = sv::launch_append(p, true, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(SV_ERR_CUDA, "append launch: %s", cudaGetErrorString(e));
+    return SV_OK;
+}
+
+size_t sv_verify_attention_q8_workspace_size(const sv_attn_desc *d) {
+    if (check_attn_desc(d) != SV_OK) return 0;
+    const int ctas = sv::attention_num_ctas();
+    if (ctas <= 0) return 0;
+    return sv::attention_q8_workspace_bytes(d->num_seqs, d->num_q_rows, d->num_q_heads, d->num_kv_heads,
+                                            d->head_dim, ctas);
+}
+
+sv_status sv_verify_attention_q8(const sv_attn_desc *d, const void *q, const sv_kv_q8 *kv,
+                                 const int32_t *block_table, const int32_t *ctx_lens,
+                                 const uint64_t *draft_mask, void *out, void *workspace,
+                                 size_t workspace_bytes, int32_t *status_flags, void *stream) {
+    sv_status s = check_attn_desc(d);
+    if (s != SV_OK) return s;
+    if (d->num_seqs == 0) return SV_OK;
+    if ((s = check_q8(kv)) != SV_OK) return s;
+    const sv_paged_kv pools = {kv->k_pool, kv->v_pool};
+    if ((s = check_attn_ptrs(q, &pools, block_table, ctx_lens, draft_mask, out, status_flags)) != SV_OK) return s;
+    const int ctas = sv::attention_num_ctas();
+    if (ctas <= 0) return fail(SV_ERR_CUDA, "cannot query the current device");
+    const size_t need = sv::attention_q8_workspace_bytes(d->num_seqs, d->num_q_rows, d->num_q_heads,
+                                                         d->num_kv_heads, d->head_dim, ctas);
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 256))
+        return fail(SV_ERR_WORKSPACE, "workspace must be 256-byte aligned and hold %zu bytes", need);
+    const sv::AttnParams p =
+        attn_params(d, q, &pools, block_table, ctx_lens, draft_mask, out, workspace, status_flags, ctas);
+    cudaError_t e = sv::launch_attention_q8(p, kv->scales, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(SV_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
+    return SV_OK;
+}
+
+sv_status sv_kv_commit_q8(const sv_attn_desc *d, int32_t num_layers, const sv_kv_q8 *layers,
+                          const int32_t *block_table, const int32_t *ctx_lens, const int32_t *accept_len,
+                          const int32_t *accept_path, int32_t *new_ctx_lens, int32_t *status_flags, void *stream) {
+    sv_status s = check_commit(d, num_layers, layers, true);
+    if (s != SV_OK) return s;
+    for (int l = 0; l < num_layers; ++l)
+        if ((s = check_q8(layers + l)) != SV_OK) return s;
+    if (d->num_seqs == 0) return SV_OK;
+    if ((s = check_commit_arrays(d, block_table, ctx_lens, accept_len, accept_path, new_ctx_lens, status_flags)) != SV_OK)
+        return s;
+    sv::CommitQ8Launch c;
+    memset(&c, 0, sizeof c);
+    c.block_table = block_table;
+    c.ctx_lens = ctx_lens;
+    c.accept_len = accept_len;
+    c.accept_path = accept_path;
+    c.new_ctx = new_ctx_lens;
+    c.status = status_flags;
+    c.B = d->num_seqs;
+    c.N = d->num_q_rows;
+    c.Hkv = d->num_kv_heads;
+    c.D = d->head_dim;
+    c.max_blocks = d->max_blocks_per_seq;
+    c.num_blocks = d->num_blocks;
+    c.L = num_layers;
+    memcpy(c.layer, layers, (size_t)num_layers * sizeof *layers);
+    cudaError_t e = sv::launch_kv_commit_q8(c, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(SV_ERR_CUDA, "kv commit launch: %s", cudaGetErrorString(e));
     return SV_OK;
 }
