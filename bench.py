@@ -81,7 +81,7 @@ def measured_peaks():
 
 # the sources the attention kernels are built from (a recorded ncu traffic
 # figure stays valid while these are unchanged)
-ATTENTION_SOURCES = ("sv_attention.cu", "sv_tc.cuh", "sv_device.cuh", "sv_internal.h")
+ATTENTION_SOURCES = ("sv_attention.cu", "sv_schedule.cuh", "sv_tc.cuh", "sv_device.cuh", "sv_internal.h")
 
 
 def _code_only(text: str) -> str:

@@ -46,16 +46,11 @@
 // Putting keys on the MMA M dimension keeps the tensor-core work at
 // 2 * 128 * RP * D per tile however few rows N*G there are, instead of
 // padding the rows to 128.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include <string.h>
 
-#include <atomic>
 #include <mutex>
 
-#include "sv_internal.h"
-#include "sv_tc.cuh"
+#include "sv_schedule.cuh"
 
 namespace sv {
 
@@ -69,124 +64,6 @@ __host__ __device__ constexpr int tc_cw(int RP) { return RP == 96 ? 32 : 16; }
 constexpr int WARPS_PER_WG = 4;
 __host__ __device__ constexpr int tc_nwg(int RP) { return RP / tc_cw(RP); }
 __host__ __device__ constexpr int tc_threads(int RP) { return 32 * (WARPS_PER_WG * tc_nwg(RP) + 4); }
-// Running column maximum of a column that has seen no visible key: finite, so
-// that s*scale - M_NONE is +huge for a visible score (it votes for a raise) and
-// -inf for a masked one (p = 0), with no special case in the exponentials.
-constexpr float M_NONE = -3.402823466e38f;
-// Drain limit: after an abort, a role still waits this long for its own copies
-// and products in flight. The limit of every other wait is AttnParams::wait_limit_ns
-// (2 s; test hooks shorten it).
-constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
-
-// ---------------------------------------------------------------------------
-// Schedule helpers (attention and combine kernels agree on these).
-// ---------------------------------------------------------------------------
-SV_DEV int seq_tiles(const AttnParams &p, int b) {
-    const int C = p.ctx_lens[b];
-    const bool ok = C >= p.N && C <= p.max_blocks * PAGE;
-    return ok ? (C + TILE_KEYS - 1) / TILE_KEYS : 0;
-}
-
-// Schedule positions of one unit of sequence b: its tiles plus UNIT_COST.
-SV_DEV int seq_slots(const AttnParams &p, int b) {
-    const int t = seq_tiles(p, b);
-    return t > 0 ? t + UNIT_COST : 0;
-}
-
-// Tiles of a sequence from its schedule positions.
-SV_DEV int real_tiles(int positions) { return positions > 0 ? positions - UNIT_COST : 0; }
-
-// Exclusive prefix of per-sequence schedule positions (seq_slots) into
-// TP[0..B] (and, when CL is given, the context lengths into CL[0..B)); the
-// whole block participates.
-SV_DEV void tile_prefix(const AttnParams &p, int *TP, int *scratch, int *CL = nullptr) {
-    const int nt = blockDim.x, tid = threadIdx.x;
-    const int per = (p.B + nt - 1) / nt;
-    const int s0 = min(tid * per, p.B), s1 = min(s0 + per, p.B);
-    int local = 0;
-    for (int b = s0; b < s1; ++b) {
-        local += seq_slots(p, b);
-        if (CL) CL[b] = p.ctx_lens[b];
-    }
-    const int lane = tid & 31, warp = tid >> 5;
-    int incl = local;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-    }
-    if (lane == 31) scratch[warp] = incl;
-    __syncthreads();
-    int wpre = 0;
-    for (int w = 0; w < warp; ++w) wpre += scratch[w];
-    int run = wpre + incl - local;
-    for (int b = s0; b < s1; ++b) {
-        TP[b] = run;
-        run += seq_slots(p, b);
-    }
-    if (tid == nt - 1) TP[p.B] = run;
-    __syncthreads();
-}
-
-// Schedule position t -> sequence b (largest b with ups*TP[b] <= t).
-SV_DEV int tile_seq(const int *TP, int B, int ups, int t) {
-    int lo = 0, hi = B;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (ups * TP[mid] <= t) lo = mid; else hi = mid;
-    }
-    return lo;
-}
-
-// A tile: sequence b, head/row-chunk hr, tile j of the unit's Tb tiles.
-struct TileInfo {
-    int b, hr, j, Tb;
-};
-
-// The tile after ti in the end-to-end order (j, then head/row chunk, then
-// sequence; sequences without tiles are skipped). Callers stop at their range's
-// end, so running past the last sequence only has to be harmless.
-SV_DEV void next_tile(TileInfo &ti, const int *TP, int B, int ups) {
-    if (++ti.j < ti.Tb) return;
-    ti.j = 0;
-    if (++ti.hr < ups) return;
-    ti.hr = 0;
-    do {
-        ++ti.b;
-        ti.Tb = ti.b < B ? real_tiles(TP[ti.b + 1] - TP[ti.b]) : 1;
-    } while (ti.b < B && ti.Tb == 0);
-}
-
-// The first tile a CTA owns and how many it owns: the tiles whose schedule
-// positions fall in [v0, v1) (positions past a unit's tiles hold no work).
-SV_DEV TileInfo cta_tiles(const int *TP, int B, int ups, int v0, int v1, int *ntiles) {
-    TileInfo ti{0, 0, 0, 1};
-    *ntiles = 0;
-    if (v0 >= v1) return ti;
-    ti.b = tile_seq(TP, B, ups, v0);
-    const int T1 = TP[ti.b + 1] - TP[ti.b];  // positions per unit of b (> 0)
-    const int off = v0 - ups * TP[ti.b];
-    ti.hr = off / T1;
-    ti.j = off - ti.hr * T1;
-    ti.Tb = real_tiles(T1);
-    if (ti.j >= ti.Tb) {  // a position past the unit's tiles: start at the next unit
-        ti.j = ti.Tb - 1;
-        next_tile(ti, TP, B, ups);
-    }
-    TileInfo w = ti;
-    int n = 0;
-    while (w.b < B) {
-        const int pos = ups * TP[w.b] + w.hr * (w.Tb + UNIT_COST) + w.j;
-        if (pos >= v1) break;
-        const int here = min(w.Tb - w.j, v1 - pos);
-        n += here;
-        w.j = w.Tb - 1;
-        next_tile(w, TP, B, ups);
-    }
-    *ntiles = n;
-    return ti;
-}
-
 // ---------------------------------------------------------------------------
 // Shared-memory plan of the tcgen05 kernel (host and device agree).
 // ---------------------------------------------------------------------------
@@ -922,6 +799,10 @@ __global__ void __launch_bounds__(32 * COMBINE_ROWS, MIN_CTAS) attn_combine_kern
     tot = block_sum_i(tot, red_i);
     before = block_sum_i(before, red_i);
     const int Tb = block_sum_i(own, red_i);
+    // every CTA waits, also one with nothing to merge: a grid of CTAs that all
+    // returned early would be over while the attention kernel still runs, and the
+    // next call's kernel, which waits for this grid, would start too soon
+    griddep_wait();  // the partials are complete and visible
     if (Tb == 0 || r >= rows) return;
     const int total = ups * tot;
     const int W = (total + p.num_ctas - 1) / p.num_ctas;
@@ -934,7 +815,6 @@ __global__ void __launch_bounds__(32 * COMBINE_ROWS, MIN_CTAS) attn_combine_kern
     const float *seg0 = p.ws_partial + (size_t)(u + first) * sf;
     const bool dl = lane < D / 4;  // this lane holds head dims 4*lane .. 4*lane+3
 
-    griddep_wait();  // the partials are complete and visible
     // one round of loads: this lane's dims of the first partials, and segment lane's (m, l)
     float4 ov[COMBINE_REG_SEGS];
 #pragma unroll
@@ -1028,7 +908,7 @@ size_t attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int num_c
     return (units + (size_t)num_ctas) * slot_floats * sizeof(float);
 }
 
-static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
@@ -1065,27 +945,6 @@ static bool encode_q_map(CUtensorMap *m, const void *q, int B, int N, int Hq, in
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-constexpr int SMEM_LIMIT = 227 * 1024;
-
-// Launch with programmatic stream serialization: the kernel may start while the
-// previous kernel in the stream finishes; it waits (griddep_wait) before it
-// reads any input or writes anything.
-template <typename... Args>
-static cudaError_t launch_programmatic(void (*kfn)(Args...), dim3 grid, dim3 block, size_t smem,
-                                       cudaStream_t stream, const Args &...args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kfn, args...);
 }
 
 template <int D, int RP>
@@ -1143,8 +1002,12 @@ cudaError_t launch_attention(const AttnParams &p, cudaStream_t stream) {
     const int RP = RU > 64 ? 96 : (RU + 15) / 16 * 16;
     cudaError_t e = p.D == 128 ? launch_tc_rp<128>(P, RP, stream) : launch_tc_rp<64>(P, RP, stream);
     if (e != cudaSuccess || p.all_slots) return e;  // a cascade call merges in the shared-prefix kernel
+    return launch_combine(p, stream);
+}
+
+cudaError_t launch_combine(const AttnParams &p, cudaStream_t stream) {
     return launch_programmatic(4 * p.units <= p.num_ctas ? attn_combine_kernel<2> : attn_combine_kernel<3>,
-                               dim3((RU + COMBINE_ROWS - 1) / COMBINE_ROWS, p.units),
+                               dim3((p.rows_unit + COMBINE_ROWS - 1) / COMBINE_ROWS, p.units),
                                dim3(32 * COMBINE_ROWS), 0, stream, p);
 }
 

@@ -40,6 +40,9 @@ SV_DEV void mbar_arrive_expect_tx(uint64_t *b, uint32_t bytes) {
                  "r"(bytes)
                  : "memory");
 }
+SV_DEV void mbar_arrive_n(uint64_t *b, uint32_t n) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(b)), "r"(n) : "memory");
+}
 SV_DEV bool mbar_try_wait(uint64_t *b, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -167,6 +170,36 @@ SV_DEV uint64_t sw128_desc(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_byte
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn_major, bool b_mn_major) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn_major ? 1u : 0u) << 15) |
            ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// The same fields for kind::f8f6f4: types 0 = e4m3, 1 = e5m2 -> fp32.
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, int a_type, int b_type, bool a_mn_major,
+                                                bool b_mn_major) {
+    return (1u << 4) | ((uint32_t)a_type << 7) | ((uint32_t)b_type << 10) | ((a_mn_major ? 1u : 0u) << 15) |
+           ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// Shared-memory matrix descriptor; swizzle: 0 none, 2 = 128-byte, 4 = 64-byte.
+// K-major: sbo = bytes between groups of 8 rows (M or N). MN-major: swizzled,
+// sbo = bytes between groups of 8 k, lbo between swizzle columns of M or N;
+// not swizzled, sbo = bytes between 16-byte groups of M or N, lbo between groups of 8 k.
+SV_DEV uint64_t smem_desc(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes, int swizzle) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)((lbo_bytes >> 4) & 0x3FFFu) << 16;
+    d |= (uint64_t)((sbo_bytes >> 4) & 0x3FFFu) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)swizzle << 61;
+    return d;
+}
+
+SV_DEV void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accum) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accum)
+        : "memory");
 }
 
 SV_DEV void mma_bf16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accum) {
