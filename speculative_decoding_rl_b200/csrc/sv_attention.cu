@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(tc_threads(RP), 1) attn_tc_kernel(const __grid
     tile_prefix(p, TP, scratch, CL);  // contains __syncthreads
     const int ups = p.Hkv * p.RC;
     const int total = ups * TP[p.B];  // schedule positions of all units
-    const int W = total > 0 ? (total + p.num_ctas - 1) / p.num_ctas : 1;
+    const int W = schedule_width(p, total);
     if (tid == 0) {
         // this CTA's tiles: those at positions [cta*W, cta*W + W); published to
         // every role through the (now free) scratch words
@@ -805,7 +805,7 @@ __global__ void __launch_bounds__(32 * COMBINE_ROWS, MIN_CTAS) attn_combine_kern
     griddep_wait();  // the partials are complete and visible
     if (Tb == 0 || r >= rows) return;
     const int total = ups * tot;
-    const int W = (total + p.num_ctas - 1) / p.num_ctas;
+    const int W = schedule_width(p, total);
     const int tpre = ups * before + hr * (Tb + UNIT_COST);
     const int first = tpre / W, n = (tpre + Tb - 1) / W - first + 1;
     if (n == 1) return;  // written by the attention kernel

@@ -14,25 +14,33 @@
 //                over the same K accumulate into S.
 //   O^T = V^T P  the weights p, rounded to fp16, are cut into three e5m2 values
 //                (3 significant bits each, fp16's own exponent range): at least
-//                9 bits, 2^-9 of the weight, down to 2^-17 of the running
-//                maximum and 2^-29 of the maximum below, so that a long flat
+//                9 bits, 2^-9 of the weight, down to 2^-14 of the running
+//                maximum and 2^-26 of the maximum below, so that a long flat
 //                tail under one large weight keeps its mass. One product takes
 //                the pieces side by side (N = 3 x rows) and the epilogue adds
 //                the three sums.
 // A key is a lane of the softmax warps, so a page's scales are one factor per
 // thread: K's joins the exponent, V's the weight before it is cut.
 //
-// Inside a CTA (tcgen05 + TMA, one persistent CTA per SM):
-//   warps 0 .. MATH_WARPS-1  softmax warpgroups, as in the bf16 kernel; at the
-//                start they also cut the first unit's query rows;
-//   WARP_K, WARP_V  TMA producers: per tile, 8 boxes of one page each;
-//   WARP_MMA     TMEM allocator and MMA issuer;
-//   WARP_ST      status flags; then the V ring: rows past ctx_len and NaN of new
-//                keys (a row of a draft tree must not meet what its mask hides)
-//                are zeroed before a tile goes to its product;
-//   WARP_Q       query pieces of the units to come, and the pages' scales, four
-//                tiles at a time, for the softmax.
+// What the stream leaves per tile is less than the softmax's chain (scores out
+// of TMEM, vote, exponentials, cut, back to shared memory) takes, so a CTA works
+// on NT tiles at once: it stands for NT work ranges of the schedule, each with
+// its own warps, rings, S, P and O. Code is kept short as well, since warps in
+// different places of a long loop wait for instructions: columns are taken 16 at
+// a time in rolled loops, and what they carry from tile to tile, the row sums,
+// stays in TMEM beside S.
+//
+// Inside a CTA (tcgen05 + TMA, one persistent CTA per SM), for each range:
+//   softmax      NG warpgroups of CW row columns; a thread is one key of the
+//                tile. They also cut their units' query rows;
+//   WARP_LD      TMA producer of K and V: per tile, 8 boxes of one page each;
+//   WARP_MMA     MMA issuer;
+//   WARP_AUX     status flags; the V ring: rows past ctx_len and NaN of new keys
+//                (a row of a draft tree must not meet what its mask hides) are
+//                zeroed before a tile goes to its product; the pages' scales.
 #include <string.h>
+
+#include <type_traits>
 
 #include "sv_page8.cuh"
 #include "sv_q8.h"
@@ -44,118 +52,150 @@ using namespace tc;
 
 namespace {
 
-// Softmax warpgroups as in the bf16 kernel: each owns q8_cw(RP) row columns.
-__host__ __device__ constexpr int q8_cw(int RP) { return RP == 96 ? 32 : 16; }
-__host__ __device__ constexpr int q8_nwg(int RP) { return RP / q8_cw(RP); }
-__host__ __device__ constexpr int q8_threads(int RP) { return 32 * (4 * q8_nwg(RP) + 5); }
-
-constexpr int SC_BATCH = 4;    // tiles whose page scales are fetched together
-constexpr int SC_RING = 4;     // batches in shared memory
-constexpr int PAGES_TILE = TILE_KEYS / PAGE;
-constexpr int UNIT_RING = 32;  // units whose NaN mark is kept
-// Units whose row scales are kept. Unit u is cut once unit u - 2 is through
-// Q.K; the softmax has then loaded S of unit u - 4 at least, may still be using
-// that unit's scales, and is past unit u - 5: five are enough.
-constexpr int QS_RING = 8;
-constexpr int MAX_RING = 8;    // K or V slots at most
-// p is held as p * 2^P_SHIFT / (V's scale): the running maximum's weight is
-// 2^12, a raise waits until one passes 2^(12 + RESCALE_LOG2), below fp16's and
-// e5m2's largest values, and fp16's smallest step is 2^-36 of the maximum.
-constexpr float P_SCALE = 4096.f, P_UNSCALE = 1.f / 4096.f;
-constexpr float RESCALE_LOG2 = 3.f;
-
-struct Q8Layout {
-    uint32_t tile_bytes, off_k, off_q, q_bytes, off_p, p_bytes, off_bar, off_tp, off_cl, off_red, off_ms, off_as,
-        off_lred, off_rowi, off_umask, off_vote, off_fin, off_mfin, off_qs, off_sc, off_vnan, off_misc, total;
+// Shape of the kernel for RP padded rows per unit.
+template <int D, int RP>
+struct Q8Shape {
+    static constexpr int CW = RP >= 64 ? 32 : RP;              // row columns per warpgroup
+    static constexpr int NG = RP / CW;                         // warpgroups per range
+    static constexpr int NT = RP == 96 ? 1 : D == 128 ? 2 : RP == 16 ? 4 : RP == 32 ? 3 : 2;  // ranges
+    // O accumulators side by side: P's pieces enter a product's N together as far
+    // as TMEM has room for their sums, the last one goes into the last sum.
+    static constexpr int ACC = RP == 64 ? 1 : RP >= 48 || NT == 3 ? 2 : 3;
+    static constexpr int SB = 2;                  // S buffers per range
+    static constexpr int PB = NT == 1 ? 2 : 1;    // P buffers per range
+    static constexpr int NQ = RP == 64 ? 1 : 2;   // query buffers per range
+    static constexpr int TM_S = (ACC * RP + 31) / 32 * 32;    // of a range's TMEM columns: O, S, row sums
+    static constexpr int TM_L = TM_S + SB * RP;
+    static constexpr int R_COLS = 512 / NT / 32 * 32;
+    static_assert(TM_L + RP <= R_COLS, "TMEM");
+    static constexpr int WGS = NT * NG;
+    static constexpr int MATH_WARPS = 4 * WGS;
+    static constexpr int THREADS = 32 * (MATH_WARPS + 3 * NT);
 };
 
-__host__ __device__ constexpr int q8_barriers(int RP, int NK, int NV) {
-    return 2 * NK + 3 * NV + 2 * 2 /*q*/ + 2 * 2 /*s*/ + 2 /*p*/ + 2 * 2 /*o*/ + 1 /*done*/ + q8_nwg(RP) +
-           2 * SC_RING;
-}
+constexpr int SC_BATCH = 4;    // tiles whose page scales are fetched together
+constexpr int SC_RING = 4;     // batches of a range in shared memory
+constexpr int PAGES_TILE = TILE_KEYS / PAGE;
+constexpr int UNIT_RING = 32;  // units of a range whose NaN mark is kept
+// Units whose row scales are kept: the warpgroups of a range cut unit u + 1
+// while the slower one may still use the scales of unit u - 1.
+constexpr int QS_RING = 4;
+constexpr int MAX_RING = 16;   // K and V slots of a range at most
+// p is held as p * P_SCALE * (V's scale): the running maximum's weight is 2^9, a
+// raise waits until one passes 2^(9 + RESCALE_LOG2), below fp16's and e5m2's
+// largest values; e5m2's smallest step is 2^-25 of the maximum.
+constexpr float P_SCALE = 512.f, P_UNSCALE = 1.f / 512.f;
+constexpr float RESCALE_LOG2 = 6.f;
+// A range is at least this long: on small calls, shorter ranges would cost the
+// combine more partials than they save.
+constexpr int MIN_WIDTH = 2;
 
-__host__ __device__ inline Q8Layout q8_layout(int D, int RP, int NK, int NV, int B) {
+struct Q8Layout {
+    uint32_t tile_bytes, off_k, off_q, q_bytes, off_p, p_bytes, off_bar, off_tp, off_cl, off_red, off_nm, off_as,
+        off_rowi, off_rowoff, off_umask, off_fin, off_qs, off_sc, off_vnan, off_misc, total;
+};
+
+template <int D, int RP>
+__host__ __device__ inline Q8Layout q8_layout(int NK, int NV, int B) {
+    using S = Q8Shape<D, RP>;
     Q8Layout L;
-    const int NWG = q8_nwg(RP), CW = q8_cw(RP);
     L.tile_bytes = (uint32_t)TILE_KEYS * D;
-    L.off_k = NV * L.tile_bytes;
-    L.off_q = L.off_k + NK * L.tile_bytes;
-    L.q_bytes = 2u * RP * D;  // two pieces
-    L.off_p = L.off_q + 2 * L.q_bytes;
-    L.p_bytes = 3u * RP * TILE_KEYS;  // three pieces
-    L.off_bar = L.off_p + 2 * L.p_bytes;
-    L.off_tp = L.off_bar + 8u * q8_barriers(RP, NK, NV);
+    L.off_k = S::NT * NV * L.tile_bytes;           // [range][NV]
+    L.off_q = L.off_k + S::NT * NK * L.tile_bytes; // [range][NK]
+    L.q_bytes = 2u * RP * D;                       // [range][NQ]: two pieces
+    L.off_p = L.off_q + S::NT * S::NQ * L.q_bytes;
+    L.p_bytes = 3u * RP * TILE_KEYS;               // [range][PB]: three pieces
+    L.off_bar = L.off_p + S::NT * S::PB * L.p_bytes;
+    const int nbar = S::NT * (2 * NK + 3 * NV + S::NQ + 2 * S::SB + 2 * S::PB + 1 + 2 * SC_RING) + S::WGS;
+    L.off_tp = L.off_bar + 8u * nbar;
     L.off_cl = L.off_tp + 4u * (B + 1);
     L.off_red = (L.off_cl + 4u * B + 15u) & ~15u;
-    L.off_ms = L.off_red + 4u * 2 * NWG * 4 * CW;   // [par][wg][warp][CW] tile column maxima
-    L.off_as = L.off_ms + 4u * 2 * RP;              // [par][RP] running maxima
-    L.off_lred = L.off_as + 4u * 2 * RP;            // [par][RP] rescale factors
-    L.off_rowi = L.off_lred + 4u * NWG * 4 * CW;    // [wg][warp][CW] row-sum partials
-    L.off_umask = (L.off_rowi + 4u * RP + 15u) & ~15u;
-    L.off_vote = L.off_umask + 8u * NWG * 64;       // [wg][64] mask words of the unit
-    L.off_fin = L.off_vote + 4u * 2 * NWG * 4;      // [par][wg][warp] rescale votes
-    L.off_mfin = L.off_fin + 4u * RP;               // [RP] row sums of a finished unit
-    L.off_qs = (L.off_mfin + 4u * RP + 15u) & ~15u;
-    L.off_sc = L.off_qs + 4u * QS_RING * RP;        // [QS_RING][RP] query row scales
-    L.off_vnan = L.off_sc + 8u * SC_RING * SC_BATCH * PAGES_TILE;  // page scales (K, V)
-    L.off_misc = L.off_vnan + 4u * UNIT_RING;
-    L.total = L.off_misc + 16u + 4u * 32;
+    L.off_nm = L.off_red + 4u * 4 * S::NT * RP;    // [range][warp][RP] tile column maxima, or row sums
+    L.off_as = L.off_nm + 4u * S::NT * RP;         // [range][RP] running maxima, negated
+    L.off_rowi = L.off_as + 4u * S::NT * RP;       // [range][RP] rescale factors
+    L.off_rowoff = (L.off_rowi + 4u * RP + 15u) & ~15u;
+    L.off_umask = L.off_rowoff + 4u * RP;
+    L.off_fin = L.off_umask + 8u * S::WGS * 64;    // [wg][64] mask words of the unit
+    L.off_qs = (L.off_fin + 4u * S::NT * RP + 15u) & ~15u;  // [range][RP] row sums of a finished unit
+    L.off_sc = L.off_qs + 4u * S::NT * QS_RING * RP;        // [range][QS_RING][RP] query row scales
+    L.off_vnan = L.off_sc + 8u * S::NT * SC_RING * SC_BATCH * PAGES_TILE;  // [range][batch][32] page scales (K, V)
+    L.off_misc = L.off_vnan + 4u * S::NT * UNIT_RING;
+    L.total = L.off_misc + 16u + 4u * 40;
     return L;
 }
 
 struct Q8Params {
     CUtensorMap tm_k;
     CUtensorMap tm_v;
-    AttnParams a;
+    AttnParams a;  // num_ctas counts ranges
     const float2 *scales;
     int NK, NV, Nc;
 };
 
-// Cuts row r of a unit's queries into two e4m3 pieces in shared memory (128- or
-// 64-byte swizzled rows of D bytes, the second piece's RP rows after the
-// first's) and writes the row's scale; one warp. A row with an entry that is
-// not finite gets the scale NaN, and with it NaN outputs.
-template <int D, int RP>
-SV_DEV void cut_query_row(const uint16_t *src, uint8_t *qbuf, float *qs, int r, int lane) {
-    constexpr int E = D / 32;  // entries per lane
+// A lane's D/16 entries of a query row, in bf16 bits, as two 8-bit words' worth of
+// registers: 16 lanes hold a row.
+template <int D>
+struct QueryLane {
+    static constexpr int E = D / 16;
+    using Half = typename std::conditional<D == 128, uint2, uint32_t>::type;  // E bytes
+    using Raw = typename std::conditional<D == 128, uint4, uint2>::type;      // 2 E bytes
+};
+
+// Cuts the entries a lane holds of row r (raw bf16 bits, the low half of them at
+// `a`, the high half at `b`) into two e4m3 pieces, the first written to `a`, the
+// second to `b`, and writes the row's scale. The 16 lanes of a half warp hold a
+// row. A row with an entry that is not finite gets the scale NaN, and with it
+// NaN outputs.
+template <int D>
+SV_DEV void cut_query_row(uint8_t *a, uint8_t *b, float *scale, int lane) {
+    constexpr int E = QueryLane<D>::E;
+    using Half = typename QueryLane<D>::Half;
+    const Half ra = *reinterpret_cast<const Half *>(a), rb = *reinterpret_cast<const Half *>(b);
+    const uint32_t *wa = reinterpret_cast<const uint32_t *>(&ra), *wb = reinterpret_cast<const uint32_t *>(&rb);
     float x[E];
-    if constexpr (E == 4) {
-        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(src) + lane);
-        x[0] = __uint_as_float(w.x << 16); x[1] = __uint_as_float(w.x & 0xFFFF0000u);
-        x[2] = __uint_as_float(w.y << 16); x[3] = __uint_as_float(w.y & 0xFFFF0000u);
-    } else {
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(src) + lane);
-        x[0] = __uint_as_float(w << 16); x[1] = __uint_as_float(w & 0xFFFF0000u);
-    }
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < E; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-    top = __reduce_max_sync(0xffffffffu, top);
+    for (int i = 0; i < E / 2; ++i) {
+        const uint32_t w = i < E / 4 ? wa[i] : wb[i - E / 4];
+        x[2 * i] = __uint_as_float(w << 16);
+        x[2 * i + 1] = __uint_as_float(w & 0xFFFF0000u);
+        top = max(top, max((w << 16) & 0x7FFFFFFFu, w & 0x7FFF0000u));
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     const bool finite = top < 0x7F800000u;
     // |x| <= 448 * 2^e. e stays where 2^-e and 2^e are normal.
     const int ex = (int)(top >> 23) - 127;
     const int e = max(-126, (top & 0x7FFFFFu) <= 0x600000u ? ex - 8 : ex - 7);
-    const float inv = exp2_int(-e);
-    uint32_t hi = 0, lo = 0;
+    const float inv = finite ? exp2_int(-e) : 0.f;
+    uint32_t hi[E / 4] = {}, lo[E / 4] = {};
 #pragma unroll
     for (int i = 0; i < E; i += 2) {
-        const float a = finite ? x[i] * inv : 0.f, b = finite ? x[i + 1] * inv : 0.f;
-        const uint32_t h = float2_to_e4m3x2(a, b);
+        const float y0 = x[i] * inv, y1 = x[i + 1] * inv;
+        const uint32_t h = float2_to_e4m3x2(y0, y1);
         const float2 back = e4m3x2_to_float2(h);
-        hi |= h << (8 * i);
-        lo |= float2_to_e4m3x2(a - back.x, b - back.y) << (8 * i);
+        hi[i / 4] |= h << (8 * (i % 4));
+        lo[i / 4] |= float2_to_e4m3x2(y0 - back.x, y1 - back.y) << (8 * (i % 4));
     }
-    const int at = lane * E;  // byte of the row
-    const int sw = D == 128 ? r & 7 : (r >> 1) & 3;
-    uint8_t *dst = qbuf + r * D + (((at >> 4) ^ sw) << 4) + (at & 15);
-    if constexpr (E == 4) {
-        *reinterpret_cast<uint32_t *>(dst) = hi;
-        *reinterpret_cast<uint32_t *>(dst + RP * D) = lo;
-    } else {
-        *reinterpret_cast<uint16_t *>(dst) = (uint16_t)hi;
-        *reinterpret_cast<uint16_t *>(dst + RP * D) = (uint16_t)lo;
+    *reinterpret_cast<Half *>(a) = *reinterpret_cast<const Half *>(hi);
+    *reinterpret_cast<Half *>(b) = *reinterpret_cast<const Half *>(lo);
+    if (lane % 16 == 0) *scale = finite ? exp2_int(e) : NAN;
+}
+
+// Sums of 16 values over the warp's lanes: the lane returns that of value
+// (lane >> 1), lanes 2c and 2c + 1 the same. Each step halves the values a lane
+// carries: 16 shuffles in place of 80.
+SV_DEV float warp_sum16(float *v, int lane) {
+#pragma unroll
+    for (int half = 8; half > 0; half >>= 1) {
+        const bool up = lane & (2 * half);
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+            const float send = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, 2 * half);
+        }
     }
-    if (lane == 0) qs[r] = finite ? exp2_int(e) : NAN;
+    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
 // fp16 pairs of four weights -> the bytes of their first 3-bit pieces (cut off
@@ -175,211 +215,228 @@ SV_DEV uint32_t cut_piece(uint32_t *h, bool last) {
     return bytes;
 }
 
+// Two fp32 operations per instruction.
+SV_DEV uint64_t pack2(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+SV_DEV void unpack2(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+SV_DEV uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+SV_DEV uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+SV_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+// The smaller of the two, NaN if a is.
+SV_DEV float fmin_nan(float a, float b) {
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// Barrier of the 128 threads of a warpgroup with the or of a predicate.
+SV_DEV bool wg_any(int id, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, %2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}\n"
+        : "=r"(r)
+        : "r"((uint32_t)v), "r"(id)
+        : "memory");
+    return r != 0;
+}
+
 template <int D, int RP>
-__global__ void __launch_bounds__(q8_threads(RP), 1) attn_q8_kernel(const __grid_constant__ Q8Params P) {
-    constexpr int NWG = q8_nwg(RP);
-    constexpr int CW = q8_cw(RP);
-    constexpr int MATH_WARPS = 4 * NWG;
-    constexpr int NTHREADS = q8_threads(RP);
-    constexpr int WARP_K = MATH_WARPS, WARP_MMA = MATH_WARPS + 1, WARP_V = MATH_WARPS + 2, WARP_ST = MATH_WARPS + 3,
-                  WARP_Q = MATH_WARPS + 4;
-    // The three pieces side by side in one product's N while two O buffers of
-    // that width fit TMEM beside S (and N = 288 is past a product's 256); for 96
-    // rows the pieces go one after the other into the same columns.
-    constexpr bool SIDE = RP <= 64;
-    constexpr int ON = SIDE ? 3 * RP : RP;           // columns of an O buffer
-    constexpr int S_COLS = (RP + 31) / 32 * 32;      // TMEM columns per S buffer
-    constexpr int O_COLS = (ON + 31) / 32 * 32;      // and per O buffer
-    constexpr int TM_O = 2 * S_COLS;
-    static_assert(TM_O + 2 * O_COLS <= 512, "TMEM");
+__global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(const __grid_constant__ Q8Params P) {
+    using S = Q8Shape<D, RP>;
+    constexpr int CW = S::CW, NG = S::NG, NT = S::NT, SB = S::SB, PB = S::PB, NQ = S::NQ;
+    constexpr int ACC = S::ACC;
+    constexpr int MATH_WARPS = S::MATH_WARPS, NTHREADS = S::THREADS;
+    constexpr int WARP_LD = MATH_WARPS, WARP_MMA = MATH_WARPS + NT, WARP_AUX = MATH_WARPS + 2 * NT;
     constexpr int SW = D == 128 ? 2 : 4;             // swizzle of K, V and Q rows
-    constexpr uint32_t PIECE = 16u * TILE_KEYS;      // bytes of one piece of 16 columns
+    constexpr uint32_t GROUP = 16u * TILE_KEYS;      // bytes of 16 columns of one piece of P
     const AttnParams &p = P.a;
     const int NK = P.NK, NV = P.NV;
-    auto qphase = [](int u) -> uint32_t { return (u >> 1) & 1; };
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    const Q8Layout L = q8_layout(D, RP, NK, NV, p.B);
+    const Q8Layout L = q8_layout<D, RP>(NK, NV, p.B);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // the range this warp works for, and its barriers
+    const int r = warp < MATH_WARPS ? warp / (4 * NG) : (warp - MATH_WARPS) % NT;
+    const int nrb = 2 * NK + 3 * NV + NQ + 2 * SB + 2 * PB + 1 + 2 * SC_RING;
     uint64_t *bar = reinterpret_cast<uint64_t *>(base + L.off_bar);
-    uint64_t *k_full = bar, *k_empty = bar + NK;
-    uint64_t *v_full = bar + 2 * NK, *v_empty = v_full + NV, *vz = v_empty + NV;
-    uint64_t *q_full = vz + NV, *q_empty = q_full + 2;
-    uint64_t *s_full = q_empty + 2, *s_empty = s_full + 2;
-    uint64_t *p_full = s_empty + 2;
-    uint64_t *o_full = p_full + 2;     // [2] by tile parity: the tile's PV has completed, its P buffer is free
-    uint64_t *o_free = o_full + 2;     // [2] by unit parity: the unit's O buffer has been read out
-    uint64_t *sc_full = o_free + 2, *sc_empty = sc_full + SC_RING;
+    uint64_t *k_full = bar + r * nrb, *k_empty = k_full + NK;
+    uint64_t *v_full = k_empty + NK, *v_empty = v_full + NV;
+    uint64_t *vz = v_empty + NV;        // [NV] the tile's V is ready for its PV
+    uint64_t *q_full = vz + NV;         // [NQ]
+    uint64_t *s_full = q_full + NQ, *s_empty = s_full + SB;
+    uint64_t *p_full = s_empty + SB;    // [PB]
+    uint64_t *o_full = p_full + PB;     // [PB] the tile's PV has completed, its P is free
+    uint64_t *sc_full = o_full + PB, *sc_empty = sc_full + SC_RING;
     uint64_t *done_bar = sc_empty + SC_RING;
-    uint64_t *wg_bar = done_bar + 1;
+    uint64_t *wg_bar = bar + NT * nrb + (warp >> 2);
     int *TP = reinterpret_cast<int *>(base + L.off_tp);
     int *CL = reinterpret_cast<int *>(base + L.off_cl);
-    float *red = reinterpret_cast<float *>(base + L.off_red);
-    float *mS = reinterpret_cast<float *>(base + L.off_ms);
-    float *aS = reinterpret_cast<float *>(base + L.off_as);
-    float *lred = reinterpret_cast<float *>(base + L.off_lred);
-    int *rowi = reinterpret_cast<int *>(base + L.off_rowi);
-    uint64_t *umask = reinterpret_cast<uint64_t *>(base + L.off_umask);
-    int *vote = reinterpret_cast<int *>(base + L.off_vote);
-    float *lfin = reinterpret_cast<float *>(base + L.off_fin);
-    float *mfin = reinterpret_cast<float *>(base + L.off_mfin);
-    float *qs = reinterpret_cast<float *>(base + L.off_qs);
-    float2 *scr = reinterpret_cast<float2 *>(base + L.off_sc);
-    int *vnan = reinterpret_cast<int *>(base + L.off_vnan);
+    int *rowi = reinterpret_cast<int *>(base + L.off_rowi);      // [RP] row r -> r / G
+    int *rowoff = reinterpret_cast<int *>(base + L.off_rowoff);  // [RP] entries from a unit's first row to row r
+    float2 *scr = reinterpret_cast<float2 *>(base + L.off_sc) + r * SC_RING * 32;
+    int *vnan = reinterpret_cast<int *>(base + L.off_vnan) + r * UNIT_RING;
+    uint8_t *k_ring = base + L.off_k + r * NK * L.tile_bytes, *v_ring = base + r * NV * L.tile_bytes;
+    uint8_t *q_buf = base + L.off_q + r * NQ * L.q_bytes, *p_buf = base + L.off_p + r * PB * L.p_bytes;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(base + L.off_misc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(base + L.off_misc + 4);
     int *scratch = reinterpret_cast<int *>(base + L.off_misc + 16);
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-
-    if (tid == 0) {
+    if (lane == 0 && warp >= WARP_AUX) {  // each range's barriers, by its AUX warp
         for (int s = 0; s < NK; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1); }
         for (int s = 0; s < NV; ++s) { mbar_init(&v_full[s], 1); mbar_init(&v_empty[s], 1); mbar_init(&vz[s], 1); }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&q_full[i], MATH_WARPS); mbar_init(&q_empty[i], 1);
-            mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], MATH_WARPS);
-            mbar_init(&p_full[i], MATH_WARPS);
-            mbar_init(&o_full[i], 1); mbar_init(&o_free[i], MATH_WARPS);
-        }
-        for (int i = 0; i < SC_RING; ++i) { mbar_init(&sc_full[i], 1); mbar_init(&sc_empty[i], MATH_WARPS); }
+        for (int i = 0; i < NQ; ++i) mbar_init(&q_full[i], 4 * NG);
+        for (int i = 0; i < SB; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], 4 * NG); }
+        for (int i = 0; i < PB; ++i) { mbar_init(&p_full[i], 4 * NG); mbar_init(&o_full[i], 1); }
+        for (int i = 0; i < SC_RING; ++i) { mbar_init(&sc_full[i], 1); mbar_init(&sc_empty[i], 4 * NG); }
         mbar_init(done_bar, 1);
-        for (int g = 0; g < NWG; ++g) mbar_init(&wg_bar[g], 4);
-        *abort_flag = 0;
+        for (int g = 0; g < NG; ++g) mbar_init(bar + NT * nrb + r * NG + g, 4);
+        if (r == 0) *abort_flag = 0;
         fence_barrier_init();
     }
     if (warp == WARP_MMA) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
-    if (warp == WARP_K && lane == 0) {
+    if (warp == WARP_LD && lane == 0) {
         tma_prefetch_desc(&P.tm_k);
         tma_prefetch_desc(&P.tm_v);
     }
-    for (int r = tid; r < RP; r += NTHREADS) {
-        rowi[r] = r / p.G;
-        for (int i = 0; i < QS_RING; ++i) qs[i * RP + r] = 1.f;
-    }
-    {  // zero both query buffers: rows past a unit's real rows stay zero
-        uint4 *q4 = reinterpret_cast<uint4 *>(base + L.off_q);
-        for (uint32_t e = tid; e < 2 * L.q_bytes / 16u; e += NTHREADS) q4[e] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < RP; i += NTHREADS) {
+        rowi[i] = i / p.G;
+        rowoff[i] = (i / p.G * p.Hq + i % p.G) * D;
     }
     griddep_wait();  // no input is read, and nothing written, before this wait
     griddep_launch_dependents();
     tile_prefix(p, TP, scratch, CL);  // contains __syncthreads
     const int ups = p.Hkv * p.RC;
     const int total = ups * TP[p.B];
-    const int W = total > 0 ? (total + p.num_ctas - 1) / p.num_ctas : 1;
-    if (tid == 0) {
-        const int v0 = min((int)blockIdx.x * W, total), v1 = min(v0 + W, total);
+    const int W = schedule_width(p, total);
+    // range r of this CTA is the schedule's range blockIdx.x + r * gridDim.x
+    if (tid < NT) {
+        const int v0 = (int)min((long long)(blockIdx.x + tid * gridDim.x) * W, (long long)total);
+        const int v1 = min(v0 + W, total);
         int n;
         const TileInfo t0 = cta_tiles(TP, p.B, ups, v0, v1, &n);
-        scratch[0] = t0.b; scratch[1] = t0.hr; scratch[2] = t0.j; scratch[3] = t0.Tb; scratch[4] = n;
+        int *o = scratch + 8 * tid;
+        o[0] = t0.b; o[1] = t0.hr; o[2] = t0.j; o[3] = t0.Tb; o[4] = n;
     }
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    const TileInfo t_first{scratch[0], scratch[1], scratch[2], scratch[3]};
-    const int ntiles = scratch[4];
+    const uint32_t tmem = *tmem_slot + r * S::R_COLS;
+    const TileInfo t_first{scratch[8 * r], scratch[8 * r + 1], scratch[8 * r + 2], scratch[8 * r + 3]};
+    const int ntiles = scratch[8 * r + 4];
 
-    // query rows of tile ti's unit, the CTA's u-th, every `step`-th from `r0` on
-    auto cut_queries = [&](const TileInfo &ti, int u, int r0, int step) {
-        const int h = ti.hr / p.RC, rc = ti.hr - h * p.RC;
-        const int rows = min(p.rows_unit, p.R - rc * p.rows_unit);
-        const uint16_t *q = p.q + (((size_t)ti.b * p.N + rc * P.Nc) * p.Hq + h * p.G) * D;
-#pragma unroll 4
-        for (int r = r0; r < rows; r += step) {
-            const int i = rowi[r];
-            cut_query_row<D, RP>(q + ((size_t)i * p.Hq + (r - i * p.G)) * D, base + L.off_q + (u & 1) * L.q_bytes,
-                                 qs + u % QS_RING * RP, r, lane);
-        }
+    auto wait_w = [&](uint64_t *b, uint32_t parity) -> bool {
+        const bool done = mbar_test(b, parity) || mbar_wait(b, parity, abort_flag, p.wait_limit_ns);
+        return __all_sync(0xffffffffu, done);
     };
 
-    if (warp == WARP_K || warp == WARP_V) {
-        // ------------------------- TMA producers --------------------------
-        if (lane == 0) {
-            const bool is_k = warp == WARP_K;
-            const int NR = is_k ? NK : NV;
-            uint64_t *full = is_k ? k_full : v_full;
-            uint64_t *empty = is_k ? k_empty : v_empty;
-            const CUtensorMap *tm = is_k ? &P.tm_k : &P.tm_v;
-            uint8_t *ring = base + (is_k ? L.off_k : 0u);
-            int issued_tiles = 0, rs = 0;
-            uint32_t rph = 0;
-            TileInfo ti = t_first;
-            for (int lt = 0; lt < ntiles; ++lt, next_tile(ti, TP, p.B, ups)) {
-                const int h = ti.hr / p.RC;
-                const int C = CL[ti.b];
-                int blks[PAGES_TILE];
-#pragma unroll
-                for (int pg = 0; pg < PAGES_TILE; ++pg) {
-                    const int page = ti.j * PAGES_TILE + pg;
-                    blks[pg] = page * PAGE < C ? __ldg(p.block_table + (size_t)ti.b * p.max_blocks + page) : -1;
-                }
-                const int s = rs;
-                if (!mbar_wait(&empty[s], rph ^ 1u, abort_flag, p.wait_limit_ns)) break;
-                if (++rs == NR) { rs = 0; rph ^= 1u; }
-                mbar_arrive_expect_tx(&full[s], L.tile_bytes);
-                uint8_t *dst = ring + s * L.tile_bytes;
-#pragma unroll
-                for (int pg = 0; pg < PAGES_TILE; ++pg) {
-                    // out of range (or past ctx_len): a coordinate past the pool, which the TMA unit fills with zeros
-                    const int blk = (blks[pg] >= 0 && blks[pg] < p.num_blocks) ? blks[pg] : p.num_blocks;
-                    tma_load_4d(dst + pg * (PAGE * D), tm, &full[s], 0, 0, h, blk);
-                }
-                issued_tiles = lt + 1;
-            }
-            if (*abort_flag)  // this CTA's own copies land before it can exit
-                for (int lt = max(0, issued_tiles - NR); lt < issued_tiles; ++lt)
-                    mbar_wait_time(&full[lt % NR], (lt / NR) & 1, WAIT_LIMIT_NS);
-        }
-    } else if (warp == WARP_ST) {
+    if (warp >= WARP_AUX) {
         // ---------------- per-sequence status (and invalid sequences) ----------------
-        for (int b = blockIdx.x; b < p.B; b += p.num_ctas) {
-            const int C = CL[b];
-            const bool ctx_ok = C >= p.N && C <= p.max_blocks * PAGE;
-            int bad = 0;
-            if (ctx_ok) {
-                for (int jb = lane; jb < (C + PAGE - 1) / PAGE; jb += 32) {
-                    const int blk = __ldg(p.block_table + (size_t)b * p.max_blocks + jb);
-                    bad |= (blk < 0 || blk >= p.num_blocks);
+        if (r == 0)
+            for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+                const int C = CL[b];
+                const bool ctx_ok = C >= p.N && C <= p.max_blocks * PAGE;
+                int bad = 0;
+                if (ctx_ok) {
+                    for (int jb = lane; jb < (C + PAGE - 1) / PAGE; jb += 32) {
+                        const int blk = __ldg(p.block_table + (size_t)b * p.max_blocks + jb);
+                        bad |= (blk < 0 || blk >= p.num_blocks);
+                    }
+                } else {
+                    uint4 *o4 = reinterpret_cast<uint4 *>(p.out + (size_t)b * p.N * p.Hq * D);
+                    for (int e = lane; e < p.N * p.Hq * D / 8; e += 32) o4[e] = make_uint4(0, 0, 0, 0);
                 }
-            } else {
-                uint4 *o4 = reinterpret_cast<uint4 *>(p.out + (size_t)b * p.N * p.Hq * D);
-                for (int e = lane; e < p.N * p.Hq * D / 8; e += 32) o4[e] = make_uint4(0, 0, 0, 0);
+                bad = __any_sync(0xffffffffu, bad);
+                if (p.status && lane == 0)
+                    p.status[b] = (ctx_ok ? 0 : SV_FLAG_BAD_CONTEXT) | (bad ? SV_FLAG_BAD_BLOCK : 0);
             }
-            bad = __any_sync(0xffffffffu, bad);
-            if (p.status && lane == 0)
-                p.status[b] = (ctx_ok ? 0 : SV_FLAG_BAD_CONTEXT) | (bad ? SV_FLAG_BAD_BLOCK : 0);
+        // Page scales come in batches of SC_BATCH tiles: lane l has tile l / 8's page
+        // l % 8. The next batch is fetched while this one's tiles are cleaned.
+        TileInfo ta = t_first;
+        int blk = -1, head = 0;
+        auto batch_ids = [&](int t) {  // of the batch whose first tile, the range's t-th, is ta
+            TileInfo mine = ta;
+#pragma unroll 1
+            for (int j = 1; j <= SC_BATCH; ++j) {
+                next_tile(ta, TP, p.B, ups);
+                if (lane / PAGES_TILE >= j) mine = ta;
+            }
+            const int page = mine.j * PAGES_TILE + lane % PAGES_TILE;
+            head = mine.hr / p.RC;
+            blk = -1;
+            if (t + lane / PAGES_TILE < ntiles && page * PAGE < CL[mine.b])
+                blk = __ldg(p.block_table + (size_t)mine.b * p.max_blocks + page);
+        };
+        float2 sc = make_float2(1.f, 1.f);
+        auto batch_scales = [&]() {
+            sc = make_float2(1.f, 1.f);
+            if (blk >= 0 && blk < p.num_blocks) sc = __ldg(P.scales + (size_t)blk * p.Hkv + head);
+        };
+        auto batch_publish = [&](int batch) -> bool {
+            const int slot = batch % SC_RING;
+            if (!wait_w(&sc_empty[slot], (batch / SC_RING & 1) ^ 1)) return false;
+            scr[slot * 32 + lane] = make_float2(fmaxf(sc.x, PAGE8_SCALE_MIN), fmaxf(sc.y, PAGE8_SCALE_MIN));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sc_full[slot]);
+            return true;
+        };
+        bool ok = true;
+        if (ntiles > 0) {
+            batch_ids(0);
+            batch_scales();
+            ok = batch_publish(0);
         }
-        // ------------------- V rows past ctx_len, NaN of new keys -------------------
-        // 0 * NaN is NaN: rows past ctx_len hold whatever the pool holds, and a new
-        // key that some rows must not see may hold NaN. Both are zeroed here once
-        // the tile has landed. Where NaN was zeroed the unit is marked, and its
-        // read-out puts it back for the rows that see the key.
+        // V rows past ctx_len, NaN of new keys. 0 * NaN is NaN: rows past ctx_len
+        // hold whatever the pool holds, and a new key that some rows must not see
+        // may hold NaN. Both are zeroed once the tile has landed. Where NaN was
+        // zeroed the unit is marked, and its read-out puts it back for the rows that
+        // see the key.
         TileInfo ti = t_first;
         int vs = 0, u = -1;
         uint32_t vph = 0;
-        for (int lt = 0; lt < ntiles; ++lt, next_tile(ti, TP, p.B, ups)) {
-            const int s = vs;
-            const uint32_t par = vph;
-            if (++vs == NV) { vs = 0; vph ^= 1u; }
+#pragma unroll 1
+        for (int lt = 0; lt < ntiles && ok; ++lt) {
+            const bool more = lt % SC_BATCH == 0 && lt + SC_BATCH < ntiles;
+            if (more) batch_ids(lt + SC_BATCH);
             if (lt == 0 || ti.j == 0) {
                 ++u;
                 // the ring outlasts the units between this warp and the read-out
                 if (lane == 0) vnan[u % UNIT_RING] = 0;
             }
-            const bool landed = mbar_test(&v_full[s], par) || mbar_wait(&v_full[s], par, abort_flag, p.wait_limit_ns);
-            if (!__all_sync(0xffffffffu, landed)) break;
             const int C = CL[ti.b];
             // keys of the tile from the first new one on, and from ctx_len on
             // (pages wholly past ctx_len were loaded as zeros by the TMA unit)
             const int kn = max(0, C - p.N - ti.j * TILE_KEYS), k0 = max(0, C - ti.j * TILE_KEYS);
             const int k1 = min(TILE_KEYS, (k0 + PAGE - 1) / PAGE * PAGE);
+            next_tile(ti, TP, p.B, ups);
+            if (!(ok = wait_w(&v_full[vs], vph))) break;
             if (kn < k1) {
-                uint8_t *vt = base + s * L.tile_bytes;
+                uint8_t *vt = v_ring + vs * L.tile_bytes;
                 bool hit = false;
+#pragma unroll 1
                 for (int e = kn * (D / 16) + lane; e < k1 * (D / 16); e += 32) {
                     uint4 *at = reinterpret_cast<uint4 *>(vt) + e;
                     if (e >= k0 * (D / 16)) {
@@ -405,237 +462,271 @@ __global__ void __launch_bounds__(q8_threads(RP), 1) attn_q8_kernel(const __grid
                 fence_proxy_async_smem();
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&vz[s]);
+            if (lane == 0) mbar_arrive(&vz[vs]);
+            if (++vs == NV) { vs = 0; vph ^= 1u; }
+            if (more) batch_scales();
+            if (lt % SC_BATCH == 2 && lt + 2 < ntiles) ok = batch_publish(lt / SC_BATCH + 1);
         }
-    } else if (warp == WARP_Q) {
-        // ------------- query pieces and page scales, ahead of their use -------------
-        TileInfo ti = t_first;
-        int u = -1, batch = 0;
-        bool ok = true;
-        for (int lt = 0; lt < ntiles && ok; ++lt, next_tile(ti, TP, p.B, ups)) {
-            if (lt % SC_BATCH == 0) {
-                // tile lt + lane / 8, page lane % 8 of it
-                TileInfo w = ti, mine = ti;
-#pragma unroll
-                for (int j = 1; j < SC_BATCH; ++j) {
-                    next_tile(w, TP, p.B, ups);
-                    if (lane / PAGES_TILE >= j) mine = w;
-                }
-                const int page = mine.j * PAGES_TILE + lane % PAGES_TILE;
-                float2 sc = make_float2(1.f, 1.f);
-                if (lt + lane / PAGES_TILE < ntiles && page * PAGE < CL[mine.b]) {
-                    const int blk = __ldg(p.block_table + (size_t)mine.b * p.max_blocks + page);
-                    if (blk >= 0 && blk < p.num_blocks) {
-                        sc = __ldg(P.scales + (size_t)blk * p.Hkv + mine.hr / p.RC);
-                        sc.x = fmaxf(sc.x, PAGE8_SCALE_MIN);
-                        sc.y = fmaxf(sc.y, PAGE8_SCALE_MIN);
-                    }
-                }
-                const int slot = batch % SC_RING;
-                const bool free = mbar_test(&sc_empty[slot], (batch / SC_RING & 1) ^ 1) ||
-                                  mbar_wait(&sc_empty[slot], (batch / SC_RING & 1) ^ 1, abort_flag, p.wait_limit_ns);
-                if (!(ok = __all_sync(0xffffffffu, free))) break;
-                scr[slot * 32 + lane] = sc;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sc_full[slot]);
-                ++batch;
-            }
-            if (lt == 0 || ti.j == 0) {
-                ++u;
-                if (u == 0) continue;  // the softmax warps cut the first unit's rows
-                const bool free = mbar_test(&q_empty[u & 1], qphase(u) ^ 1) ||
-                                  mbar_wait(&q_empty[u & 1], qphase(u) ^ 1, abort_flag, p.wait_limit_ns);
-                if (!(ok = __all_sync(0xffffffffu, free))) break;
-                cut_queries(ti, u, 0, 1);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_n(&q_full[u & 1], MATH_WARPS);
-            }
-        }
-    } else if (warp == WARP_MMA) {
+    } else if (warp >= WARP_MMA) {
         // -------------------------- MMA issuer ----------------------------
-        // Polls both queues and issues whichever product is ready, as in the bf16 kernel.
+        // The range's products in order.
         if (lane == 0) {
             constexpr uint32_t idq = idesc_f8(128, RP, 0, 0, false, false);
-            constexpr uint32_t idp = idesc_f8(128, ON, 0, 1, true, true);
-            int nq = 0, np = 0, lu = -1, lup = -1;
+            constexpr uint32_t idp = idesc_f8(128, ACC * RP, 0, 1, true, true), idp1 = idesc_f8(128, RP, 0, 1, true, true);
+            const uint64_t kdesc = smem_desc(smem_u32(k_ring), 16, 8 * D, SW);
+            const uint64_t qdesc = smem_desc(smem_u32(q_buf), 16, 8 * D, SW);
+            // D = 64: dims 64..127 of the 128-row product read bytes of other keys and are not read out
+            const uint64_t vdesc = smem_desc(smem_u32(v_ring), 8 * D, 8 * D, SW);
+            const uint64_t pdesc = smem_desc(smem_u32(p_buf), 128, GROUP, 0);
+            // addresses stay in a descriptor's low word; the high words (K's and Q's are alike) are fixed
+            const uint32_t khi = (uint32_t)(kdesc >> 32), vhi = (uint32_t)(vdesc >> 32), phi = (uint32_t)(pdesc >> 32);
             int ks = 0, vs = 0;
             uint32_t kph = 0, vph = 0;
-            const uint64_t kdesc = smem_desc(smem_u32(base + L.off_k), 16, 8 * D, SW);
-            const uint64_t qdesc = smem_desc(smem_u32(base + L.off_q), 16, 8 * D, SW);
-            // D = 64: dims 64..127 of the 128-row product read bytes of other keys and are not read out
-            const uint64_t vdesc = smem_desc(smem_u32(base), 8 * D, 8 * D, SW);
-            const uint64_t pdesc = smem_desc(smem_u32(base + L.off_p), 128, SIDE ? PIECE : 3 * PIECE, 0);
-            TileInfo tq = t_first;
-            TileInfo tp = tq;
-            uint32_t idle = 0;
-            uint64_t idle_since = 0;
-            while (np < ntiles) {
-                bool progressed = false;
-                if (nq < ntiles) {
-                    const bool newu = (nq == 0 || tq.j == 0);
-                    const int lu_n = newu ? lu + 1 : lu;
-                    const int sb = nq & 1;
-                    if ((!newu || mbar_test(&q_full[lu_n & 1], qphase(lu_n))) && mbar_test(&k_full[ks], kph) &&
-                        mbar_test(&s_empty[sb], ((nq >> 1) & 1) ^ 1)) {
-                        lu = lu_n;
-                        tc_fence_after();
-                        const uint64_t ka = kdesc + ((ks * L.tile_bytes) >> 4);
-                        const uint64_t qa = qdesc + (((lu & 1) * L.q_bytes) >> 4);
-#pragma unroll
-                        for (int kk = 0; kk < D / 32; ++kk)
-#pragma unroll
-                            for (int piece = 0; piece < 2; ++piece)
-                                mma_f8_ss(tmem + sb * S_COLS, ka + ((kk * 32) >> 4),
-                                          qa + ((piece * RP * D + kk * 32) >> 4), idq, kk + piece > 0);
-                        mma_commit(&s_full[sb]);
-                        mma_commit(&k_empty[ks]);
-                        if (nq == ntiles - 1 || tq.j == tq.Tb - 1) mma_commit(&q_empty[lu & 1]);
-                        if (++ks == NK) { ks = 0; kph ^= 1u; }
-                        ++nq;
-                        if (nq < ntiles) next_tile(tq, TP, p.B, ups);
-                        progressed = true;
-                    }
+            TileInfo tq = t_first, tp = tq;
+            int lu = -1;
+            auto wait1 = [&](uint64_t *b, uint32_t parity) {
+                return mbar_test(b, parity) || mbar_wait(b, parity, abort_flag, p.wait_limit_ns);
+            };
+            auto issue_qk = [&](int t) -> bool {
+                if (t == 0 || tq.j == 0) {
+                    ++lu;
+                    if (!wait1(&q_full[lu % NQ], (lu / NQ) & 1)) return false;
                 }
-                if (np < nq) {
-                    const bool newu = (np == 0 || tp.j == 0);
-                    const int lup_n = newu ? lup + 1 : lup;
-                    const int pb = np & 1, ob = lup_n & 1;
-                    if (mbar_test(&p_full[pb], (np >> 1) & 1) && mbar_test(&vz[vs], vph) &&
-                        (!newu || mbar_test(&o_free[ob], ((lup_n >> 1) & 1) ^ 1))) {
-                        lup = lup_n;
-                        tc_fence_after();
-                        const uint64_t va = vdesc + ((vs * L.tile_bytes) >> 4);
-                        const uint64_t pa = pdesc + ((pb * L.p_bytes) >> 4);
-                        constexpr int NPROD = SIDE ? 1 : 3;
+                if (!wait1(&k_full[ks], kph) || !wait1(&s_empty[t % SB], ((t / SB) & 1) ^ 1)) return false;
+                tc_fence_after();
+                const uint32_t ka = (uint32_t)kdesc + ((ks * L.tile_bytes) >> 4);
+                const uint32_t qa = (uint32_t)qdesc + ((lu % NQ * L.q_bytes) >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < TILE_KEYS / 32; ++kk)
+                for (int kk = 0; kk < D / 32; ++kk)
 #pragma unroll
-                            for (int piece = 0; piece < NPROD; ++piece)
-                                mma_f8_ss(tmem + TM_O + ob * O_COLS, va + ((kk * 32 * D) >> 4),
-                                          pa + ((piece * PIECE + kk * 512) >> 4), idp,
-                                          (kk + piece > 0 || !newu) ? 1u : 0u);
-                        mma_commit(&o_full[pb]);
-                        mma_commit(&v_empty[vs]);
-                        if (++vs == NV) { vs = 0; vph ^= 1u; }
-                        ++np;
-                        if (np < ntiles) next_tile(tp, TP, p.B, ups);
-                        progressed = true;
-                    }
+                    for (int piece = 0; piece < 2; ++piece)
+                        mma_f8_ss(tmem + S::TM_S + t % SB * RP, ka + ((kk * 32) >> 4), khi,
+                                  qa + ((piece * RP * D + kk * 32) >> 4), khi, idq, kk + piece > 0);
+                mma_commit(&s_full[t % SB]);
+                mma_commit(&k_empty[ks]);
+                if (++ks == NK) { ks = 0; kph ^= 1u; }
+                next_tile(tq, TP, p.B, ups);
+                return true;
+            };
+            auto issue_pv = [&](int t) -> bool {
+                const bool newu = t == 0 || tp.j == 0;
+                if (!wait1(&p_full[t % PB], (t / PB) & 1) || !wait1(&vz[vs], vph)) return false;
+                tc_fence_after();
+                const uint32_t va = (uint32_t)vdesc + ((vs * L.tile_bytes) >> 4);
+                const uint32_t pa = (uint32_t)pdesc + ((t % PB * L.p_bytes) >> 4);
+                // the first ACC pieces side by side, the others into the last sum
+#pragma unroll
+                for (int kk = 0; kk < TILE_KEYS / 32; ++kk) {
+                    mma_f8_ss(tmem, va + ((kk * 32 * D) >> 4), vhi, pa + ((kk * 512) >> 4), phi, idp,
+                              (kk > 0 || !newu) ? 1u : 0u);
+#pragma unroll
+                    for (int piece = ACC; piece < 3; ++piece)
+                        mma_f8_ss(tmem + (ACC - 1) * RP, va + ((kk * 32 * D) >> 4), vhi,
+                                  pa + ((piece * (RP / 16) * GROUP + kk * 512) >> 4), phi, idp1, 1u);
                 }
-                if (progressed) {
-                    idle = 0;
-                } else if (++idle > 8 && (__nanosleep(20), (idle & 63) == 0)) {
-                    if (*abort_flag) break;
-                    const uint64_t now = globaltimer_ns();
-                    if (idle == 64) idle_since = now;
-                    else if (now - idle_since > p.wait_limit_ns) { *abort_flag = 1; break; }
-                }
+                mma_commit(&o_full[t % PB]);
+                mma_commit(&v_empty[vs]);
+                if (++vs == NV) { vs = 0; vph ^= 1u; }
+                next_tile(tp, TP, p.B, ups);
+                return true;
+            };
+            // Q.K of tile q runs up to SB tiles ahead of P.V of tile v. With one query
+            // buffer a unit's rows are cut after the last unit is read out: its last
+            // P.V comes first.
+            int q = 0, v = 0;
+            bool ok = true;
+#pragma unroll 1
+            while (v < ntiles && ok) {
+                const bool behind = NQ == 1 && tq.j == 0 && q > v;
+                if (q < ntiles && q < v + SB && !behind)
+                    ok = issue_qk(q++);
+                else
+                    ok = issue_pv(v++);
             }
-            mma_commit(done_bar);  // every MMA of this CTA has finished before TMEM is freed
+            mma_commit(done_bar);  // every MMA of this range has finished before TMEM is freed
             mbar_wait_time(done_bar, 0, WAIT_LIMIT_NS);
+        }
+    } else if (warp >= WARP_LD) {
+        // -------------------------- TMA producer --------------------------
+        // K one tile ahead of V. Page ids of a tile, one per lane 0..7; num_blocks
+        // (a coordinate past the pool, which the TMA unit fills with zeros) for ids
+        // out of range and pages past ctx_len.
+        TileInfo ti = t_first;  // the tile after the last one whose ids were fetched
+        auto page_ids = [&]() -> int {
+            const int page = ti.j * PAGES_TILE + lane;
+            int blk = -1;
+            if (lane < PAGES_TILE && page * PAGE < CL[ti.b])
+                blk = __ldg(p.block_table + (size_t)ti.b * p.max_blocks + page);
+            return blk;
+        };
+        int slot[2] = {0, 0}, issued[2] = {0, 0};
+        uint32_t ph[2] = {0, 0};
+        bool ok = true;
+        auto load = [&](int kv, int ids, int h) -> bool {
+            uint64_t *full = kv ? v_full : k_full, *empty = kv ? v_empty : k_empty;
+            const int s = slot[kv], NR = kv ? NV : NK;
+            if (!wait_w(&empty[s], ph[kv] ^ 1u)) return false;
+            uint8_t *dst = (kv ? v_ring : k_ring) + s * L.tile_bytes;
+            if (lane == 0) mbar_arrive_expect_tx(&full[s], L.tile_bytes);
+            __syncwarp();
+            const int blk = ids >= 0 && ids < p.num_blocks ? ids : p.num_blocks;
+            if (lane < PAGES_TILE)
+                tma_load_4d(dst + lane * (PAGE * D), kv ? &P.tm_v : &P.tm_k, &full[s], 0, 0, h, blk);
+            ++issued[kv];
+            if (++slot[kv] == NR) { slot[kv] = 0; ph[kv] ^= 1u; }
+            return true;
+        };
+        int idv = 0, hv = 0;  // of the tile whose V comes next
+        int idk = 0;
+        if (ntiles > 0) idk = page_ids();
+#pragma unroll 1
+        for (int lt = 0; lt <= ntiles && ok; ++lt) {
+            const int h = ti.hr / p.RC, ids = idk;
+            if (lt < ntiles) next_tile(ti, TP, p.B, ups);
+            if (lt + 1 < ntiles) idk = page_ids();  // in flight while this tile waits for its slots
+            if (lt < ntiles) ok = load(0, ids, h);
+            if (lt > 0 && ok) ok = load(1, idv, hv);
+            idv = ids;
+            hv = h;
+        }
+        if (*abort_flag && lane == 0) {  // this range's own copies land before the CTA can exit
+            for (int i = max(0, issued[0] - NK); i < issued[0]; ++i)
+                mbar_wait_time(&k_full[i % NK], (i / NK) & 1, WAIT_LIMIT_NS);
+            for (int i = max(0, issued[1] - NV); i < issued[1]; ++i)
+                mbar_wait_time(&v_full[i % NV], (i / NV) & 1, WAIT_LIMIT_NS);
         }
     } else {
         // ------------------------------ softmax ------------------------------
-        const int wg = warp >> 2;          // warpgroup: owns row columns [wg*CW, wg*CW + CW)
+        // A wait that runs out leaves `ok` false; the warp goes on to the next vote
+        // without work, and the warpgroup leaves together from there, so that no
+        // warp is missing at a barrier.
+        const int wg = warp >> 2, cg = wg - r * NG;
         const int wiw = warp & 3;          // warp within the warpgroup = TMEM lane quadrant
         const int ell = wiw * 32 + lane;   // key (S) / head dim (O) lane
-        const int col0 = wg * CW;
-        uint32_t wg_phase = 0;
-        const uint32_t lane_base = tmem + ((uint32_t)(wiw * 32) << 16);
-        float lsum[CW];
-#pragma unroll
-        for (int c = 0; c < CW; ++c) lsum[c] = 0.f;
+        const int col0 = cg * CW;
+        const int seg = blockIdx.x + r * gridDim.x;
+        const uint32_t tm_o = tmem + ((uint32_t)(wiw * 32) << 16) + col0;
+        const uint32_t tm_s = tmem + ((uint32_t)(wiw * 32) << 16) + S::TM_S + col0, tm_l = tm_s + SB * RP;
+        float *red = reinterpret_cast<float *>(base + L.off_red) + r * 4 * RP + col0;  // [warp] * RP
+        float *nm = reinterpret_cast<float *>(base + L.off_nm) + r * RP + col0;
+        float *as = reinterpret_cast<float *>(base + L.off_as) + r * RP + col0;
+        float *lfin = reinterpret_cast<float *>(base + L.off_fin) + r * RP + col0;
+        uint64_t *umask = reinterpret_cast<uint64_t *>(base + L.off_umask) + wg * 64;
+        float *qs_ring = reinterpret_cast<float *>(base + L.off_qs) + r * QS_RING * RP;
         const size_t slot_floats = slot_stride(p.rows_unit, D);
+        uint32_t wg_phase = 0;
         bool ok = true;
-
-        int cur_u = -1, last_par = 0, lu = -1;
-        int ub = 0, uh = 0, urc = 0, uC = 0, urows = 0;
+        int lu = -1, ub = 0, uhr = 0, uC = 0;
 
         auto warp_arrive = [&](uint64_t *b) {
             __syncwarp();
             if (lane == 0) mbar_arrive(b);
         };
-        auto wait_w = [&](uint64_t *b, uint32_t parity) -> bool {
-            const bool r = mbar_test(b, parity) || mbar_wait(b, parity, abort_flag, p.wait_limit_ns);
-            return __all_sync(0xffffffffu, r);
-        };
         auto wg_sync = [&]() -> bool {
-            warp_arrive(&wg_bar[wg]);
-            const bool r = wait_w(&wg_bar[wg], wg_phase);
+            warp_arrive(wg_bar);
+            const bool done = wait_w(wg_bar, wg_phase);
             wg_phase ^= 1;
-            return r;
+            return done;
         };
-
-        if (ntiles > 0) {
-            cut_queries(t_first, 0, warp, MATH_WARPS);
-            fence_proxy_async_smem();
-            warp_arrive(&q_full[0]);
-        }
-
-        // Unit ends as in the bf16 kernel: close_unit reduces the row sums,
-        // finish_unit reads O out once the next unit's first tile is through softmax.
-        bool pending = false;
-        int pend_u = 0, pend_lu = 0, pend_jt = 0;
-        auto close_unit = [&](int jt_last) -> bool {
+        // this warpgroup's share of the query rows of tile ti's unit, the range's u-th
+        auto cut_queries = [&](const TileInfo &ti, int u) {
+            const int h = ti.hr / p.RC, rc = ti.hr - h * p.RC;
+            const int rows = min(p.rows_unit, p.R - rc * p.rows_unit);
+            const uint16_t *q = p.q + (((size_t)ti.b * p.N + rc * P.Nc) * p.Hq + h * p.G) * D;
+            // half a warp to a row; all loads in flight, then the raw bits to where the
+            // lane's pieces go, then (rolled, for the code's size) the cut in place
+            constexpr int E = QueryLane<D>::E;
+            using Raw = typename QueryLane<D>::Raw;
+            using Half = typename QueryLane<D>::Half;
+            const int row0 = (cg * 4 + wiw) * 2 + (lane >> 4), l16 = lane & 15;
+            uint8_t *qb = q_buf + u % NQ * L.q_bytes;
+            auto place = [&](int row) -> uint8_t * {
+                const int at = l16 * E, sw = D == 128 ? row & 7 : (row >> 1) & 3;
+                return qb + row * D + (((at >> 4) ^ sw) << 4) + (at & 15);
+            };
+            Raw raw[CW / 8];
 #pragma unroll
-            for (int c = 0; c < CW; ++c) {
-                const float v = warp_sum(lsum[c]);
-                if (lane == 0) lred[(wg * 4 + wiw) * CW + c] = v;
-                lsum[c] = 0.f;
+            for (int k = 0; k < CW / 8; ++k) {
+                const int row = row0 + k * 8 * NG;
+                if (row < rows) raw[k] = __ldg(reinterpret_cast<const Raw *>(q + rowoff[row]) + l16);
+                else memset(&raw[k], 0, sizeof(Raw));
             }
-            if (!wg_sync()) return false;
-            if (wiw == 0 && lane < CW) {
-                float l = 0.f;
-                for (int w = 0; w < 4; ++w) l += lred[(wg * 4 + w) * CW + lane];
-                lfin[col0 + lane] = l;
-                mfin[col0 + lane] = mS[last_par * RP + col0 + lane];
+#pragma unroll
+            for (int k = 0; k < CW / 8; ++k) {
+                uint8_t *at = place(row0 + k * 8 * NG);
+                *reinterpret_cast<Half *>(at) = reinterpret_cast<const Half *>(&raw[k])[0];
+                *reinterpret_cast<Half *>(at + RP * D) = reinterpret_cast<const Half *>(&raw[k])[1];
             }
-            if (!wg_sync()) return false;
-            pending = true;
-            pend_u = cur_u;
-            pend_lu = lu;
-            pend_jt = jt_last;
-            return true;
+#pragma unroll 1
+            for (int k = 0; k < CW / 8; ++k) {
+                const int row = row0 + k * 8 * NG;
+                uint8_t *at = place(row);
+                cut_query_row<D>(at, at + RP * D, qs_ring + u % QS_RING * RP + row, lane);
+            }
+            fence_proxy_async_smem();
+            warp_arrive(&q_full[u % NQ]);
         };
-        auto finish_unit = [&]() -> bool {
-            pending = false;
-            if (!wait_w(&o_full[pend_jt & 1], (pend_jt >> 1) & 1)) return false;
+        // The unit is through: its row sums over the 128 key lanes, then O^T (lane =
+        // head dim, column = row) out of TMEM; normalised and written out if this
+        // range covered the unit whole, else a partial for the combine kernel.
+        auto finish_unit = [&](int tlast) -> bool {
+#pragma unroll 1
+            for (int c0 = 0; c0 < CW; c0 += 16) {
+                float l[16];
+                tmem_ld16(tm_l + c0, l);
+                tmem_wait_ld();
+                const float v = warp_sum16(l, lane);
+                if (!(lane & 1)) red[wiw * RP + c0 + (lane >> 1)] = v;
+            }
+            if (!wg_sync()) return false;
+            const int fh = uhr / p.RC, frc = uhr - fh * p.RC;
+            const int frows = min(p.rows_unit, p.R - frc * p.rows_unit) - col0;  // of this warpgroup's columns
+            const int Tb = real_tiles(TP[ub + 1] - TP[ub]);
+            const int tpre = ups * TP[ub] + uhr * (Tb + UNIT_COST);  // the unit's first position
+            const bool to_slot = (tpre + Tb - 1) / W != tpre / W;
+            float *slot = p.ws_partial + (size_t)(ub * ups + uhr + seg) * slot_floats;
+            if (ell < CW) {
+                const float l = (red[ell] + red[RP + ell]) + (red[2 * RP + ell] + red[3 * RP + ell]);
+                // what O is multiplied by: a row that saw nothing gives 0
+                lfin[ell] = to_slot ? 1.f : l > 0.f || l != l ? 1.f / l : 0.f;
+                if (to_slot && ell < frows) {
+                    slot[(size_t)p.rows_unit * D + col0 + ell] = -nm[ell];
+                    slot[(size_t)p.rows_unit * D + p.rows_unit + col0 + ell] = l;
+                }
+            }
+            if (!wg_sync() || !wait_w(&o_full[tlast % PB], (tlast / PB) & 1)) return false;
             tc_fence_after();
-            const int fb = pend_u / ups, fhr = pend_u - fb * ups;
-            const int fh = fhr / p.RC, frc = fhr - fh * p.RC;
-            const int frows = min(p.rows_unit, p.R - frc * p.rows_unit);
-            const int Tb = real_tiles(TP[fb + 1] - TP[fb]);
-            const int tpre = ups * TP[fb] + fhr * (Tb + UNIT_COST);  // the unit's first position
-            const int first_cta = tpre / W;
-            const int nseg = (tpre + Tb - 1) / W - first_cta + 1;
-            const bool to_slot = nseg > 1;
-            const bool marked = vnan[pend_lu % UNIT_RING] != 0;
-            float *slot = p.ws_partial + (size_t)(pend_u + blockIdx.x) * slot_floats;
+            const bool marked = vnan[lu % UNIT_RING] != 0;
+            uint16_t *ounit = p.out + (((size_t)ub * p.N + frc * P.Nc) * p.Hq + fh * p.G) * D + ell;
+            float *sunit = slot + (size_t)col0 * D + ell;
 #pragma unroll 1
             for (int c0 = 0; c0 < CW; c0 += 16) {
                 float o[16];
-                const uint32_t oaddr = lane_base + TM_O + (pend_lu & 1) * O_COLS + (col0 + c0) * (SIDE ? 3 : 1);
-                tmem_ld16(oaddr, o);
-                if constexpr (SIDE) {
-                    float o1[16], o2[16];
-                    tmem_ld16(oaddr + 16, o1);
-                    tmem_ld16(oaddr + 32, o2);
+                tmem_ld16(tm_o + c0, o);
+#pragma unroll
+                for (int i = 1; i < ACC; ++i) {
+                    float o1[16];
+                    tmem_ld16(tm_o + i * RP + c0, o1);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) o[c] = (o[c] + (o1[c] + o2[c])) * P_UNSCALE;
-                } else {
-                    tmem_wait_ld();
+                    for (int c = 0; c < 16; ++c) o[c] += o1[c];
+                }
+                tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) o[c] *= P_UNSCALE;
+                for (int c4 = 0; c4 < 4; ++c4) {
+                    const float4 f = reinterpret_cast<const float4 *>(lfin + c0)[c4];
+                    o[c4 * 4] = o[c4 * 4] * P_UNSCALE * f.x;
+                    o[c4 * 4 + 1] = o[c4 * 4 + 1] * P_UNSCALE * f.y;
+                    o[c4 * 4 + 2] = o[c4 * 4 + 2] * P_UNSCALE * f.z;
+                    o[c4 * 4 + 3] = o[c4 * 4 + 3] * P_UNSCALE * f.w;
                 }
                 if (ell >= D) continue;
                 if (marked) {
                     // NaN among the new keys' V, zeroed for the product: back to the rows that see the key
 #pragma unroll 1
-                    for (int n = 0; n < p.N; ++n) {
-                        const int t = CL[fb] - p.N + n;
-                        const int blk = __ldg(p.block_table + (size_t)fb * p.max_blocks + t / PAGE);
+                    for (int k = 0; k < p.N; ++k) {
+                        const int t = uC - p.N + k;
+                        const int blk = __ldg(p.block_table + (size_t)ub * p.max_blocks + t / PAGE);
                         if (blk < 0 || blk >= p.num_blocks) continue;
                         const uint8_t *vp = reinterpret_cast<const uint8_t *>(p.v_pool) +
                                             (((size_t)blk * p.Hkv + fh) * PAGE + t % PAGE) * D;
@@ -643,221 +734,219 @@ __global__ void __launch_bounds__(q8_threads(RP), 1) attn_q8_kernel(const __grid
 #pragma unroll
                         for (int c = 0; c < 16; ++c) {
                             const int i = frc * P.Nc + rowi[col0 + c0 + c];
-                            if (col0 + c0 + c < frows &&
-                                (p.mask ? (__ldg(p.mask + (size_t)fb * p.N + i) >> n & 1) != 0 : n <= i))
+                            if (c0 + c < frows &&
+                                (p.mask ? (__ldg(p.mask + (size_t)ub * p.N + i) >> k & 1) != 0 : k <= i))
                                 o[c] = NAN;
                         }
                     }
+                    __syncwarp();
                 }
-                if (!to_slot) {
-                    uint16_t *orow = p.out + (((size_t)fb * p.N + frc * P.Nc) * p.Hq + fh * p.G) * D + ell;
-                    const size_t hqd = (size_t)p.Hq * D;
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        const int r = col0 + c0 + c;
-                        if (r < frows) {
-                            const int i = rowi[r];
-                            const float l = lfin[r];
-                            const __nv_bfloat16 v = __float2bfloat16_rn(l > 0.f || l != l ? __fdividef(o[c], l) : 0.f);
-                            orow[i * hqd + (size_t)(r - i * p.G) * D] = *reinterpret_cast<const uint16_t *>(&v);
-                        }
-                    }
-                } else {
+                if (to_slot) {
 #pragma unroll
                     for (int c = 0; c < 16; ++c)
-                        if (col0 + c0 + c < frows) slot[(size_t)(col0 + c0 + c) * D + ell] = o[c];
+                        if (c0 + c < frows) sunit[(c0 + c) * D] = o[c];
+                } else {
+#pragma unroll
+                    for (int c4 = 0; c4 < 4; ++c4) {
+                        const int4 at = reinterpret_cast<const int4 *>(rowoff + col0 + c0)[c4];
+                        const int off[4] = {at.x, at.y, at.z, at.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const __nv_bfloat16 v = __float2bfloat16_rn(o[c4 * 4 + i]);
+                            if (c0 + c4 * 4 + i < frows) ounit[off[i]] = *reinterpret_cast<const uint16_t *>(&v);
+                        }
+                    }
                 }
             }
-            tc_fence_before();
-            warp_arrive(&o_free[pend_lu & 1]);
-            if (to_slot && wiw == 0 && lane < CW && col0 + lane < frows) {
-                slot[(size_t)p.rows_unit * D + col0 + lane] = mfin[col0 + lane];
-                slot[(size_t)p.rows_unit * D + p.rows_unit + col0 + lane] = lfin[col0 + lane];
-            }
+            tc_fence_before();  // the next unit's first P.V, after this warpgroup's P, overwrites O
             return true;
         };
 
-        // one pass past the last tile closes and finishes the CTA's last unit
+        if (ntiles > 0) cut_queries(t_first, 0);
         TileInfo tnext = t_first;
-        for (int lt = 0; lt <= ntiles && ok; ++lt) {
+#pragma unroll 1
+        for (int lt = 0; lt <= ntiles; ++lt) {
             const bool end = lt == ntiles;
-            const TileInfo ti = end ? TileInfo{0, 0, 0, 1} : tnext;
-            if (!end) next_tile(tnext, TP, p.B, ups);
-            const bool first = (lt == 0 || ti.j == 0 || end);
+            const TileInfo ti = tnext;
+            const bool first = lt == 0 || end || ti.j == 0;
             if (first) {
-                if (lt > 0 && !(ok = close_unit(lt - 1))) break;
-                if (end) {
-                    if (pending) ok = finish_unit();
-                    break;
-                }
+                if (lt > 0 && ok) ok = finish_unit(lt - 1);
+                if (end) break;
                 ++lu;
-                cur_u = ti.b * ups + ti.hr;
                 ub = ti.b;
-                uh = ti.hr / p.RC;
-                urc = ti.hr - uh * p.RC;
+                uhr = ti.hr;
                 uC = CL[ub];
-                urows = min(p.rows_unit, p.R - urc * p.rows_unit);
+                if (NQ == 1 && lu > 0) cut_queries(ti, lu);
                 if (p.mask) {
-                    for (int k = wiw * 32 + lane; k < p.N; k += 128)
-                        umask[wg * 64 + k] = __ldg(p.mask + (size_t)ub * p.N + k);
-                    if (!(ok = wg_sync())) break;
+                    for (int k = ell; k < p.N; k += 128) umask[k] = __ldg(p.mask + (size_t)ub * p.N + k);
+                    if (ok) ok = wg_sync();
                 }
             }
-            const int sb = lt & 1, par = lt & 1;
+            next_tile(tnext, TP, p.B, ups);
             // the page's scales: K's in the exponent's unit, V's
-            const int batch = lt / SC_BATCH;
-            if (!(ok = wait_w(&sc_full[batch % SC_RING], batch / SC_RING & 1))) break;
-            const float2 scl = scr[(batch % SC_RING) * 32 + lt % SC_BATCH * PAGES_TILE + ell / PAGE];
-            if (lt % SC_BATCH == SC_BATCH - 1) warp_arrive(&sc_empty[batch % SC_RING]);
-            const float ksc = scl.x * p.scale_log2, vsc = scl.y * P_SCALE, lv = __log2f(scl.y);
-            if (!(ok = wait_w(&s_full[sb], (lt >> 1) & 1))) break;
+            const int sslot = lt / SC_BATCH % SC_RING;
+            if (ok) ok = wait_w(&sc_full[sslot], lt / (SC_BATCH * SC_RING) & 1);
+            const float2 scl = scr[sslot * 32 + lt % SC_BATCH * PAGES_TILE + ell / PAGE];
+            if (lt % SC_BATCH == SC_BATCH - 1) warp_arrive(&sc_empty[sslot]);
+            const float lv = __log2f(scl.y), ks1 = scl.x * p.scale_log2;
+            const uint64_t ksc = pack2(ks1, ks1);
+            const uint64_t vsc = pack2(scl.y * P_SCALE, scl.y * P_SCALE);
+            const float *qs = qs_ring + lu % QS_RING * RP + col0;
+            const int sb = lt % SB;
+            const uint32_t saddr = tm_s + sb * RP;
+            if (ok) ok = wait_w(&s_full[sb], (lt / SB) & 1);
             tc_fence_after();
-            float sv[CW];
-            tmem_ld_cols<CW>(lane_base + sb * S_COLS + col0, sv);
-            tmem_wait_ld();
-            tc_fence_before();
-            warp_arrive(&s_empty[sb]);
 
+            // Tiles with keys past ctx_len or new (masked) keys: -inf, back into S, for
+            // the columns that do not see this key.
             const int key = ti.j * TILE_KEYS + ell;
-            const bool valid = key < uC;
             const int newk = key - (uC - p.N);
+            if (ok && __any_sync(0xffffffffu, newk >= 0)) {
+                const int ibase = (uhr % p.RC) * P.Nc;
+#pragma unroll 1
+                for (int c0 = 0; c0 < CW; c0 += 16) {
+                    float x[16];
+                    tmem_ld16(saddr + c0, x);
+                    tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < CW; ++c) sv[c] *= ksc;
-            if (__any_sync(0xffffffffu, !valid || newk >= 0)) {
-                // tile holds keys past ctx_len or new (masked) keys: per-element visibility
-                const int ibase = urc * P.Nc;
-#pragma unroll
-                for (int c = 0; c < CW; ++c) {
-                    bool vis = valid;
-                    if (valid && newk >= 0 && col0 + c < urows) {
-                        const int i = ibase + rowi[col0 + c];
-                        vis = p.mask ? ((umask[wg * 64 + i] >> newk) & 1ull) != 0 : newk <= i;
+                    for (int c = 0; c < 16; ++c) {
+                        // columns past the unit's rows: any answer will do
+                        const int i = min(ibase + rowi[col0 + c0 + c], p.N - 1);
+                        const bool bit = p.mask ? (umask[i] >> (newk & 63) & 1ull) != 0 : newk <= i;
+                        if (newk >= 0 && !(bit && key < uC)) x[c] = -INFINITY;
                     }
-                    if (!vis) sv[c] = -INFINITY;
+                    tmem_st16(saddr + c0, x);
                 }
+                tmem_wait_st();
             }
 
             // x = s * qs is the exponent (log2 units, without the maximum); the
-            // running maximum is of x + log2(V's scale), the weight that enters
-            // the product with V. It is raised only when one passes it by
-            // 2^RESCALE_LOG2, by a vote of the warpgroup, as in the bf16 kernel.
-            const float4 *qs4 = reinterpret_cast<const float4 *>(qs + lu % QS_RING * RP + col0);
-            const float4 *mo4 = reinterpret_cast<const float4 *>(mS + (par ^ 1) * RP + col0);
-            bool need = first;
-            if (!first) {
-                const float thr = RESCALE_LOG2 - lv;
-#pragma unroll
-                for (int c4 = 0; c4 < CW / 4; ++c4) {
-                    const float4 m4 = mo4[c4], q4 = qs4[c4];
-                    need |= fmaf(sv[c4 * 4 + 0], q4.x, -m4.x) > thr;
-                    need |= fmaf(sv[c4 * 4 + 1], q4.y, -m4.y) > thr;
-                    need |= fmaf(sv[c4 * 4 + 2], q4.z, -m4.z) > thr;
-                    need |= fmaf(sv[c4 * 4 + 3], q4.w, -m4.w) > thr;
-                }
-            }
-            const bool wneed = __any_sync(0xffffffffu, need);
-            if (lane == 0) vote[(par * NWG + wg) * 4 + wiw] = wneed;
-            if (!(ok = wg_sync())) break;
-            const int *vt = vote + (par * NWG + wg) * 4;
-            const bool rescale = (vt[0] | vt[1] | vt[2] | vt[3]) != 0;
-            if (rescale) {
-                float *rd = red + ((par * NWG + wg) * 4 + wiw) * CW;
-                const float *qr = qs + lu % QS_RING * RP + col0;
-#pragma unroll
-                for (int c = 0; c < CW; ++c) {
-                    float m;
-                    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(fmaf(sv[c], qr[c], lv)));
-                    if (lane == c) rd[c] = m;
-                }
-                if (!(ok = wg_sync())) break;
-                if (wiw == 0 && lane < CW) {
-                    const int c = lane;
-                    const float m_old = first ? M_NONE : mS[(par ^ 1) * RP + col0 + c];
-                    float rmax = -INFINITY;
-                    for (int w = 0; w < 4; ++w) rmax = fmaxf(rmax, red[((par * NWG + wg) * 4 + w) * CW + c]);
-                    const float mx = fmaxf(m_old, rmax);  // stays M_NONE while nothing is visible
-                    mS[par * RP + col0 + c] = mx;
-                    aS[par * RP + col0 + c] = ex2_approx(m_old - mx);  // M_NONE - finite underflows to 0
-                }
-                if (!(ok = wg_sync())) break;
-                {
-                    const float4 *an4 = reinterpret_cast<const float4 *>(aS + par * RP + col0);
-#pragma unroll
-                    for (int c4 = 0; c4 < CW / 4; ++c4) {
-                        const float4 a4 = an4[c4];
-                        lsum[c4 * 4 + 0] *= a4.x;
-                        lsum[c4 * 4 + 1] *= a4.y;
-                        lsum[c4 * 4 + 2] *= a4.z;
-                        lsum[c4 * 4 + 3] *= a4.w;
-                    }
-                }
-                if (!first) {
-                    // scale the unit's O^T columns once the previous tile's PV has landed
-                    if (!(ok = wait_w(&o_full[(lt - 1) & 1], ((lt - 1) >> 1) & 1))) break;
-                    tc_fence_after();
+            // running maximum is of x + log2(V's scale), the weight that enters the
+            // product with V. It is raised only when one passes it by
+            // 2^RESCALE_LOG2. That is rare after a unit's first tile, so the tile's
+            // weights are made against the maxima there are, and only then does the
+            // warpgroup vote; if one was too large the maxima are raised and the tile
+            // is done again. A weight past the bound counts as the bound until then, so
+            // that its part of the row sum can be taken out again.
+            const int pb = lt % PB;
+            const float bound = RESCALE_LOG2 - lv;
+            uint8_t *pdst = p_buf + pb * L.p_bytes + (col0 / 16) * GROUP + ell * 16;
+            if (lt >= PB && ok) ok = wait_w(&o_full[pb], ((lt - PB) / PB) & 1);  // P is free
+            const bool fresh = first;
+            bool raise = first, leave = false;
+            while (true) {
+                if (!raise) {
+                    float top = -INFINITY;
+                    if (ok) {
 #pragma unroll 1
-                    for (int c0 = 0; c0 < CW; c0 += 16) {
-#pragma unroll 1
-                        for (int piece = 0; piece < (SIDE ? 3 : 1); ++piece) {
-                            float o[16];
-                            const uint32_t oaddr = lane_base + TM_O + (lu & 1) * O_COLS +
-                                                   (col0 + c0) * (SIDE ? 3 : 1) + piece * 16;
-                            tmem_ld16(oaddr, o);
+                        for (int c0 = 0; c0 < CW; c0 += 16) {
+                            float x[16], l[16];
+                            tmem_ld16(saddr + c0, x);
+                            if (fresh) {
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) l[c] = 0.f;
+                            } else {
+                                tmem_ld16(tm_l + c0, l);
+                            }
                             tmem_wait_ld();
-                            const float4 *a4p = reinterpret_cast<const float4 *>(aS + par * RP + col0 + c0);
+                            uint32_t piece[3][4];
 #pragma unroll
                             for (int c4 = 0; c4 < 4; ++c4) {
-                                const float4 a4 = a4p[c4];
-                                o[c4 * 4 + 0] *= a4.x;
-                                o[c4 * 4 + 1] *= a4.y;
-                                o[c4 * 4 + 2] *= a4.z;
-                                o[c4 * 4 + 3] *= a4.w;
+                                const ulonglong2 q4 = reinterpret_cast<const ulonglong2 *>(qs + c0)[c4];
+                                const ulonglong2 m4 = reinterpret_cast<const ulonglong2 *>(nm + c0)[c4];
+                                uint32_t h[2];
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    const int c = c4 * 4 + 2 * i;
+                                    float a, b;
+                                    unpack2(fma2(mul2(pack2(x[c], x[c + 1]), ksc), i ? q4.y : q4.x, i ? m4.y : m4.x), a, b);
+                                    top = fmaxf(fmaxf(top, a), b);
+                                    const uint64_t w = pack2(ex2_approx(fmin_nan(a, bound)), ex2_approx(fmin_nan(b, bound)));
+                                    unpack2(add2(pack2(l[c], l[c + 1]), w), l[c], l[c + 1]);
+                                    unpack2(mul2(w, vsc), a, b);
+                                    const __half2 hh = __floats2half2_rn(a, b);
+                                    h[i] = *reinterpret_cast<const uint32_t *>(&hh);
+                                }
+                                piece[0][c4] = cut_piece(h, false);
+                                piece[1][c4] = cut_piece(h, false);
+                                piece[2][c4] = cut_piece(h, true);
                             }
-                            tmem_st16(oaddr, o);
+                            tmem_st16(tm_l + c0, l);
+#pragma unroll
+                            for (int j = 0; j < 3; ++j)
+                                *reinterpret_cast<uint4 *>(pdst + (j * (RP / 16) + c0 / 16) * GROUP) =
+                                    make_uint4(piece[j][0], piece[j][1], piece[j][2], piece[j][3]);
                         }
+                        tmem_wait_st();
                     }
-                    tmem_wait_st();
-                    tc_fence_before();
+                    raise = wg_any(1 + wg, !ok || top > bound);
+                    if (!raise) break;
                 }
-            } else if (wiw == 0 && lane < CW) {
-                // keep the maxima: readers of these slots are past the next tile's vote sync
-                mS[par * RP + col0 + lane] = mS[(par ^ 1) * RP + col0 + lane];
-            }
-            last_par = par;
-            const float4 *ms4 = reinterpret_cast<const float4 *>(mS + (rescale ? par : par ^ 1) * RP + col0);
-            if (!(ok = wait_w(&o_full[sb], ((lt >> 1) & 1) ^ 1))) break;  // P buffer sb is free
-            uint8_t *pbuf = base + L.off_p + sb * L.p_bytes + ell * 16;
+                if ((leave = wg_any(1 + wg, !ok))) break;
+                // tile column maxima over the 128 keys; this tile's weights out of the row sums
+#pragma unroll 1
+                for (int c0 = 0; c0 < CW; c0 += 16) {
+                    float y[16], l[16], mine = 0.f;
+                    tmem_ld16(saddr + c0, y);
+                    if (!fresh) tmem_ld16(tm_l + c0, l);
+                    tmem_wait_ld();
 #pragma unroll
-            for (int c16 = 0; c16 < CW; c16 += 16) {
-                uint32_t piece[3][4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int c4 = c16 / 4 + k;
-                    const float4 m4 = ms4[c4], q4 = qs4[c4];
-                    const float mm[4] = {m4.x, m4.y, m4.z, m4.w}, qq[4] = {q4.x, q4.y, q4.z, q4.w};
-                    float pp[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int c = c4 * 4 + i;
-                        const float w = ex2_approx(fmaf(sv[c], qq[i], -mm[i]));
-                        lsum[c] += w;
-                        pp[i] = w * vsc;
+                    for (int c = 0; c < 16; ++c) {
+                        const float e = y[c] * ks1;
+                        float m;
+                        asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(fmaf(e, qs[c0 + c], lv)));
+                        if (lane == c) mine = m;
+                        if (!fresh) l[c] -= ex2_approx(fmin_nan(fmaf(e, qs[c0 + c], nm[c0 + c]), bound));
                     }
-                    const __half2 h0 = __floats2half2_rn(pp[0], pp[1]), h1 = __floats2half2_rn(pp[2], pp[3]);
-                    uint32_t h[2] = {*reinterpret_cast<const uint32_t *>(&h0), *reinterpret_cast<const uint32_t *>(&h1)};
-                    piece[0][k] = cut_piece(h, false);
-                    piece[1][k] = cut_piece(h, false);
-                    piece[2][k] = cut_piece(h, true);
+                    if (!fresh) tmem_st16(tm_l + c0, l);
+                    if (lane < 16) red[wiw * RP + c0 + lane] = mine;
                 }
+                tmem_wait_st();
+                ok = wg_sync();
+                if (ell < CW) {
+                    const float m_old = fresh ? M_NONE : -nm[ell];
+                    const float rmax = fmaxf(fmaxf(red[ell], red[RP + ell]), fmaxf(red[2 * RP + ell], red[3 * RP + ell]));
+                    const float mx = fmaxf(m_old, rmax);  // stays M_NONE while nothing is visible
+                    nm[ell] = -mx;
+                    as[ell] = ex2_approx(m_old - mx);  // M_NONE - finite underflows to 0
+                }
+                if (ok) ok = wg_sync();
+                if (!fresh) {
+                    // the row sums and O^T's columns follow, once the previous tile's PV has landed
+                    if (ok) ok = wait_w(&o_full[(lt - 1) % PB], ((lt - 1) / PB) & 1);
+                    tc_fence_after();
+                    if (ok) {
+#pragma unroll 1
+                        for (int i = 0; i < CW / 16 * (ACC + 1); ++i) {
+                            const int c0 = i / (ACC + 1) * 16, k = i % (ACC + 1);
+                            const uint32_t at = k == ACC ? tm_l + c0 : tm_o + k * RP + c0;
+                            float o[16];
+                            tmem_ld16(at, o);
+                            tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 3; ++j)
-                    *reinterpret_cast<uint4 *>(pbuf + ((col0 + c16) / 16 * 3 + j) * PIECE) =
-                        make_uint4(piece[j][0], piece[j][1], piece[j][2], piece[j][3]);
+                            for (int c = 0; c < 16; ++c) o[c] *= as[c0 + c];
+                            tmem_st16(at, o);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                raise = false;
             }
+            if (leave) break;
+            tc_fence_before();
             fence_proxy_async_smem();
-            warp_arrive(&p_full[sb]);
-            // the previous unit's last PV was issued before this tile's
-            if (pending && !(ok = finish_unit())) break;
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&s_empty[sb]);
+                mbar_arrive(&p_full[pb]);
+            }
+            if (NQ == 2 && first && lt + ti.Tb - ti.j < ntiles) {
+                // the next unit's query rows; the buffer's last products are those of the unit before this one
+                TileInfo nu = ti;
+                nu.j = nu.Tb - 1;
+                next_tile(nu, TP, p.B, ups);
+                cut_queries(nu, lu + 1);
+            }
         }
     }
 
@@ -889,19 +978,21 @@ bool encode_pool_q8(CUtensorMap *m, const void *pool, int num_blocks, int Hkv, i
 
 template <int D, int RP>
 cudaError_t launch_q8(Q8Params &P, cudaStream_t stream) {
+    using S = Q8Shape<D, RP>;
     // as many K and V slots as fit, V's the larger half (its slots are held longer)
-    int NK = MAX_RING, NV = MAX_RING;
-    while (q8_layout(D, RP, NK, NV, P.a.B).total + 1024 > (uint32_t)SMEM_LIMIT) {
-        if (NK >= NV) --NK; else --NV;
-        if (NK < 2) return cudaErrorInvalidConfiguration;
-    }
-    P.NK = NK;
-    P.NV = NV;
-    const size_t smem = q8_layout(D, RP, NK, NV, P.a.B).total + 1024;
+    int slots = MAX_RING;
+    while (q8_layout<D, RP>(slots / 2, slots - slots / 2, P.a.B).total + 1024 > (uint32_t)SMEM_LIMIT)
+        if (--slots < 2) return cudaErrorInvalidConfiguration;
+    P.NK = slots / 2;
+    P.NV = slots - slots / 2;
+    const size_t smem = q8_layout<D, RP>(P.NK, P.NV, P.a.B).total + 1024;
     auto kfn = attn_q8_kernel<D, RP>;
     cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_programmatic(kfn, dim3(P.a.num_ctas), dim3(q8_threads(RP)), smem, stream, P);
+    const int sms = P.a.num_ctas;
+    P.a.num_ctas = sms * S::NT;
+    e = launch_programmatic(kfn, dim3(sms), dim3(S::THREADS), smem, stream, P);
+    return e != cudaSuccess ? e : launch_combine(P.a, stream);
 }
 
 template <int D>
@@ -919,13 +1010,14 @@ cudaError_t launch_q8_rp(Q8Params &P, int RP, cudaStream_t stream) {
 }  // namespace
 
 size_t attention_q8_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int num_ctas) {
-    return attention_workspace_bytes(B, N, Hq, Hkv, D, num_ctas);
+    return attention_workspace_bytes(B, N, Hq, Hkv, D, num_ctas * Q8Shape<64, 16>::NT);
 }
 
 cudaError_t launch_attention_q8(const AttnParams &p, const float *scales, cudaStream_t stream) {
     Q8Params P;
     memset(&P, 0, sizeof P);
     P.a = p;
+    P.a.min_width = MIN_WIDTH;
     P.scales = reinterpret_cast<const float2 *>(scales);
     int RU, RC;
     row_chunks(p.N, p.G, &RU, &RC, &P.Nc);
@@ -933,8 +1025,7 @@ cudaError_t launch_attention_q8(const AttnParams &p, const float *scales, cudaSt
         !encode_pool_q8(&P.tm_v, p.v_pool, p.num_blocks, p.Hkv, p.D))
         return cudaErrorInvalidValue;
     const int RP = RU > 64 ? 96 : (RU + 15) / 16 * 16;
-    cudaError_t e = p.D == 128 ? launch_q8_rp<128>(P, RP, stream) : launch_q8_rp<64>(P, RP, stream);
-    return e != cudaSuccess ? e : launch_combine(p, stream);
+    return p.D == 128 ? launch_q8_rp<128>(P, RP, stream) : launch_q8_rp<64>(P, RP, stream);
 }
 
 }  // namespace sv

@@ -68,7 +68,8 @@ struct AttnParams {
     float *ws_partial;         // partial slots (see slot_stride)
     int B, N, Hq, Hkv, D, G, R, RC, rows_unit, max_blocks, num_blocks;
     int units;                 // B * Hkv * RC
-    int num_ctas;
+    int num_ctas;              // work ranges the schedule is cut into
+    int min_width;             // shortest range, in schedule positions (0: none)
     float scale_log2;          // log2(e) / sqrt(D)
     // Cascade call: every unit leaves its partial in a slot and no combine
     // kernel runs; the shared-prefix kernel that follows merges each row.

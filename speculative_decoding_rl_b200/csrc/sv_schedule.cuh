@@ -69,6 +69,11 @@ SV_DEV void tile_prefix(const AttnParams &p, int *TP, int *scratch, int *CL = nu
     __syncthreads();
 }
 
+// Positions of a work range.
+SV_DEV int schedule_width(const AttnParams &p, int total) {
+    return max(max(1, p.min_width), (total + p.num_ctas - 1) / p.num_ctas);
+}
+
 // Schedule position t -> sequence b (largest b with ups*TP[b] <= t).
 SV_DEV int tile_seq(const int *TP, int B, int ups, int t) {
     int lo = 0, hi = B;

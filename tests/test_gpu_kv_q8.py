@@ -237,6 +237,14 @@ def test_attention_many_short_sequences():
     check_attend(1, 4, 2, 64, lens, seed=36)
 
 
+@pytest.mark.parametrize("N,Hq,Hkv", [(3, 8, 2), (8, 12, 4), (10, 20, 4), (15, 8, 2), (11, 64, 8), (40, 12, 2)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_several_units_to_a_range(N, Hq, Hkv, D):
+    # 12 to 240 rows per KV head, units of one to three tiles, more of them than an SM's work ranges
+    lens = [N + (53 * b) % 300 for b in range(200)]
+    check_attend(N, Hq, Hkv, D, lens, seed=46)
+
+
 @pytest.mark.parametrize("lo,hi,q_scale", [(-100, -99, 2.0 ** 90), (90, 101, 2.0 ** -105), (-60, 60, 2.0 ** -62)])
 def test_attention_far_scales(lo, hi, q_scale):
     # scales at both ends of their range, and pages whose scales differ by up to 2^120
