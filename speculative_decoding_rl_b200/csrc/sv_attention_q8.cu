@@ -14,8 +14,8 @@
 //                over the same K accumulate into S.
 //   O^T = V^T P  the weights p, rounded to fp16, are cut into three e5m2 values
 //                (3 significant bits each, fp16's own exponent range): at least
-//                9 bits, 2^-9 of the weight, down to 2^-14 of the running
-//                maximum and 2^-26 of the maximum below, so that a long flat
+//                9 bits, 2^-9 of the weight, down to 2^-15 of the running
+//                maximum and 2^-24 of the maximum below, so that a long flat
 //                tail under one large weight keeps its mass. One product takes
 //                the pieces side by side (N = 3 x rows) and the epilogue adds
 //                the three sums.
@@ -57,6 +57,7 @@ template <int D, int RP>
 struct Q8Shape {
     static constexpr int CW = RP >= 64 ? 32 : RP;              // row columns per warpgroup
     static constexpr int NG = RP / CW;                         // warpgroups per range
+    static constexpr int CH = CW % 16 ? 8 : 16;                // columns taken at a time
     static constexpr int NT = RP == 96 ? 1 : D == 128 ? 2 : RP == 16 ? 4 : RP == 32 ? 3 : 2;  // ranges
     // O accumulators side by side: P's pieces enter a product's N together as far
     // as TMEM has room for their sums, the last one goes into the last sum.
@@ -81,11 +82,10 @@ constexpr int UNIT_RING = 32;  // units of a range whose NaN mark is kept
 // while the slower one may still use the scales of unit u - 1.
 constexpr int QS_RING = 4;
 constexpr int MAX_RING = 16;   // K and V slots of a range at most
-// p is held as p * P_SCALE * (V's scale): the running maximum's weight is 2^9, a
-// raise waits until one passes 2^(9 + RESCALE_LOG2), below fp16's and e5m2's
-// largest values; e5m2's smallest step is 2^-25 of the maximum.
-constexpr float P_SCALE = 512.f, P_UNSCALE = 1.f / 512.f;
-constexpr float RESCALE_LOG2 = 6.f;
+// p is held as p * P_SCALE * (V's scale): the running maximum's weight is 2^7, a
+// raise waits until one passes P_MAX = 2^15, below fp16's and e5m2's largest
+// values; half of e5m2's smallest step is 2^-24 of the maximum.
+constexpr float P_SCALE = 128.f, P_UNSCALE = 1.f / 128.f, P_MAX = 32768.f;
 // A range is at least this long: on small calls, shorter ranges would cost the
 // combine more partials than they save.
 constexpr int MIN_WIDTH = 2;
@@ -182,20 +182,33 @@ SV_DEV void cut_query_row(uint8_t *a, uint8_t *b, float *scale, int lane) {
     if (lane % 16 == 0) *scale = finite ? exp2_int(e) : NAN;
 }
 
-// Sums of 16 values over the warp's lanes: the lane returns that of value
-// (lane >> 1), lanes 2c and 2c + 1 the same. Each step halves the values a lane
-// carries: 16 shuffles in place of 80.
-SV_DEV float warp_sum16(float *v, int lane) {
+// Sums of CH (8 or 16) values over the warp's lanes: the lane returns that of
+// value lane / (32 / CH). Each step halves the values a lane carries: 16 shuffles
+// in place of 80 for 16 values.
+template <int CH>
+SV_DEV float warp_sums(float *v, int lane) {
 #pragma unroll
-    for (int half = 8; half > 0; half >>= 1) {
-        const bool up = lane & (2 * half);
+    for (int half = CH / 2, bit = 16; half > 0; half >>= 1, bit >>= 1) {
+        const bool up = lane & bit;
 #pragma unroll
         for (int i = 0; i < half; ++i) {
             const float send = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, 2 * half);
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
         }
     }
-    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+#pragma unroll
+    for (int bit = 16 / CH; bit > 0; bit >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], bit);
+    return v[0];
+}
+
+// CH columns of TMEM, 8 or 16.
+template <int CH>
+SV_DEV void tmem_load(uint32_t at, float *v) {
+    if constexpr (CH == 16) tmem_ld16(at, v); else tmem_ld8(at, v);
+}
+template <int CH>
+SV_DEV void tmem_store(uint32_t at, const float *v) {
+    if constexpr (CH == 16) tmem_st16(at, v); else tmem_st8(at, v);
 }
 
 // fp16 pairs of four weights -> the bytes of their first 3-bit pieces (cut off
@@ -238,11 +251,16 @@ SV_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     return d;
 }
 
-// The smaller of the two, NaN if a is.
-SV_DEV float fmin_nan(float a, float b) {
-    float d;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-    return d;
+// Bounded wait on a phase, in few instructions (there are two dozen of them in
+// the kernel): gives up after WAIT_TRIES tries, each of which the hardware
+// suspends for a while, or once another thread has raised *abort; raises it then.
+constexpr uint32_t WAIT_TRIES = 1u << 23;
+SV_DEV bool wait_phase(uint64_t *b, uint32_t parity, volatile int *abort) {
+    bool done = mbar_try_wait(b, parity);
+#pragma unroll 1
+    for (uint32_t i = 0; !done && i < WAIT_TRIES && !*abort; ++i) done = mbar_try_wait(b, parity);
+    if (!done) *abort = 1;
+    return done;
 }
 
 // Barrier of the 128 threads of a warpgroup with the or of a predicate.
@@ -262,7 +280,7 @@ SV_DEV bool wg_any(int id, bool v) {
 template <int D, int RP>
 __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(const __grid_constant__ Q8Params P) {
     using S = Q8Shape<D, RP>;
-    constexpr int CW = S::CW, NG = S::NG, NT = S::NT, SB = S::SB, PB = S::PB, NQ = S::NQ;
+    constexpr int CW = S::CW, NG = S::NG, NT = S::NT, SB = S::SB, PB = S::PB, NQ = S::NQ, CH = S::CH;
     constexpr int ACC = S::ACC;
     constexpr int MATH_WARPS = S::MATH_WARPS, NTHREADS = S::THREADS;
     constexpr int WARP_LD = MATH_WARPS, WARP_MMA = MATH_WARPS + NT, WARP_AUX = MATH_WARPS + 2 * NT;
@@ -302,7 +320,9 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
     int *scratch = reinterpret_cast<int *>(base + L.off_misc + 16);
 
     if (lane == 0 && warp >= WARP_AUX) {  // each range's barriers, by its AUX warp
+#pragma unroll 1
         for (int s = 0; s < NK; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1); }
+#pragma unroll 1
         for (int s = 0; s < NV; ++s) { mbar_init(&v_full[s], 1); mbar_init(&v_empty[s], 1); mbar_init(&vz[s], 1); }
         for (int i = 0; i < NQ; ++i) mbar_init(&q_full[i], 4 * NG);
         for (int i = 0; i < SB; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], 4 * NG); }
@@ -321,6 +341,7 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
         tma_prefetch_desc(&P.tm_k);
         tma_prefetch_desc(&P.tm_v);
     }
+#pragma unroll 1
     for (int i = tid; i < RP; i += NTHREADS) {
         rowi[i] = i / p.G;
         rowoff[i] = (i / p.G * p.Hq + i % p.G) * D;
@@ -349,24 +370,26 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
     const int ntiles = scratch[8 * r + 4];
 
     auto wait_w = [&](uint64_t *b, uint32_t parity) -> bool {
-        const bool done = mbar_test(b, parity) || mbar_wait(b, parity, abort_flag, p.wait_limit_ns);
-        return __all_sync(0xffffffffu, done);
+        return __all_sync(0xffffffffu, wait_phase(b, parity, abort_flag));
     };
 
     if (warp >= WARP_AUX) {
         // ---------------- per-sequence status (and invalid sequences) ----------------
         if (r == 0)
+#pragma unroll 1
             for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
                 const int C = CL[b];
                 const bool ctx_ok = C >= p.N && C <= p.max_blocks * PAGE;
                 int bad = 0;
                 if (ctx_ok) {
+#pragma unroll 1
                     for (int jb = lane; jb < (C + PAGE - 1) / PAGE; jb += 32) {
                         const int blk = __ldg(p.block_table + (size_t)b * p.max_blocks + jb);
                         bad |= (blk < 0 || blk >= p.num_blocks);
                     }
                 } else {
                     uint4 *o4 = reinterpret_cast<uint4 *>(p.out + (size_t)b * p.N * p.Hq * D);
+#pragma unroll 1
                     for (int e = lane; e < p.N * p.Hq * D / 8; e += 32) o4[e] = make_uint4(0, 0, 0, 0);
                 }
                 bad = __any_sync(0xffffffffu, bad);
@@ -485,7 +508,7 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
             TileInfo tq = t_first, tp = tq;
             int lu = -1;
             auto wait1 = [&](uint64_t *b, uint32_t parity) {
-                return mbar_test(b, parity) || mbar_wait(b, parity, abort_flag, p.wait_limit_ns);
+                return wait_phase(b, parity, abort_flag);
             };
             auto issue_qk = [&](int t) -> bool {
                 if (t == 0 || tq.j == 0) {
@@ -590,8 +613,10 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
             hv = h;
         }
         if (*abort_flag && lane == 0) {  // this range's own copies land before the CTA can exit
+#pragma unroll 1
             for (int i = max(0, issued[0] - NK); i < issued[0]; ++i)
                 mbar_wait_time(&k_full[i % NK], (i / NK) & 1, WAIT_LIMIT_NS);
+#pragma unroll 1
             for (int i = max(0, issued[1] - NV); i < issued[1]; ++i)
                 mbar_wait_time(&v_full[i % NV], (i / NV) & 1, WAIT_LIMIT_NS);
         }
@@ -644,22 +669,25 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
                 const int at = l16 * E, sw = D == 128 ? row & 7 : (row >> 1) & 3;
                 return qb + row * D + (((at >> 4) ^ sw) << 4) + (at & 15);
             };
-            Raw raw[CW / 8];
+            constexpr int PER = (RP / 2 + 4 * NG - 1) / (4 * NG);  // rows of a half warp
+            Raw raw[PER];
 #pragma unroll
-            for (int k = 0; k < CW / 8; ++k) {
+            for (int k = 0; k < PER; ++k) {
                 const int row = row0 + k * 8 * NG;
                 if (row < rows) raw[k] = __ldg(reinterpret_cast<const Raw *>(q + rowoff[row]) + l16);
                 else memset(&raw[k], 0, sizeof(Raw));
             }
 #pragma unroll
-            for (int k = 0; k < CW / 8; ++k) {
+            for (int k = 0; k < PER; ++k) {
+                if (RP % (8 * NG) && row0 + k * 8 * NG >= RP) break;
                 uint8_t *at = place(row0 + k * 8 * NG);
                 *reinterpret_cast<Half *>(at) = reinterpret_cast<const Half *>(&raw[k])[0];
                 *reinterpret_cast<Half *>(at + RP * D) = reinterpret_cast<const Half *>(&raw[k])[1];
             }
 #pragma unroll 1
-            for (int k = 0; k < CW / 8; ++k) {
+            for (int k = 0; k < PER; ++k) {
                 const int row = row0 + k * 8 * NG;
+                if (RP % (8 * NG) && row - (lane >> 4) >= RP) break;  // the warp's two rows are even and odd, RP is even
                 uint8_t *at = place(row);
                 cut_query_row<D>(at, at + RP * D, qs_ring + u % QS_RING * RP + row, lane);
             }
@@ -671,12 +699,12 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
         // range covered the unit whole, else a partial for the combine kernel.
         auto finish_unit = [&](int tlast) -> bool {
 #pragma unroll 1
-            for (int c0 = 0; c0 < CW; c0 += 16) {
-                float l[16];
-                tmem_ld16(tm_l + c0, l);
+            for (int c0 = 0; c0 < CW; c0 += CH) {
+                float l[CH];
+                tmem_load<CH>(tm_l + c0, l);
                 tmem_wait_ld();
-                const float v = warp_sum16(l, lane);
-                if (!(lane & 1)) red[wiw * RP + c0 + (lane >> 1)] = v;
+                const float v = warp_sums<CH>(l, lane);
+                if (lane % (32 / CH) == 0) red[wiw * RP + c0 + lane / (32 / CH)] = v;
             }
             if (!wg_sync()) return false;
             const int fh = uhr / p.RC, frc = uhr - fh * p.RC;
@@ -700,20 +728,20 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
             uint16_t *ounit = p.out + (((size_t)ub * p.N + frc * P.Nc) * p.Hq + fh * p.G) * D + ell;
             float *sunit = slot + (size_t)col0 * D + ell;
 #pragma unroll 1
-            for (int c0 = 0; c0 < CW; c0 += 16) {
-                float o[16];
-                tmem_ld16(tm_o + c0, o);
+            for (int c0 = 0; c0 < CW; c0 += CH) {
+                float o[CH];
+                tmem_load<CH>(tm_o + c0, o);
 #pragma unroll
                 for (int i = 1; i < ACC; ++i) {
-                    float o1[16];
-                    tmem_ld16(tm_o + i * RP + c0, o1);
+                    float o1[CH];
+                    tmem_load<CH>(tm_o + i * RP + c0, o1);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) o[c] += o1[c];
+                    for (int c = 0; c < CH; ++c) o[c] += o1[c];
                 }
                 tmem_wait_ld();
 #pragma unroll
-                for (int c4 = 0; c4 < 4; ++c4) {
+                for (int c4 = 0; c4 < CH / 4; ++c4) {
                     const float4 f = reinterpret_cast<const float4 *>(lfin + c0)[c4];
                     o[c4 * 4] = o[c4 * 4] * P_UNSCALE * f.x;
                     o[c4 * 4 + 1] = o[c4 * 4 + 1] * P_UNSCALE * f.y;
@@ -732,7 +760,7 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
                                             (((size_t)blk * p.Hkv + fh) * PAGE + t % PAGE) * D;
                         if ((vp[ell] & 0x7F) != 0x7F) continue;
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) {
+                        for (int c = 0; c < CH; ++c) {
                             const int i = frc * P.Nc + rowi[col0 + c0 + c];
                             if (c0 + c < frows &&
                                 (p.mask ? (__ldg(p.mask + (size_t)ub * p.N + i) >> k & 1) != 0 : k <= i))
@@ -743,11 +771,11 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
                 }
                 if (to_slot) {
 #pragma unroll
-                    for (int c = 0; c < 16; ++c)
+                    for (int c = 0; c < CH; ++c)
                         if (c0 + c < frows) sunit[(c0 + c) * D] = o[c];
                 } else {
 #pragma unroll
-                    for (int c4 = 0; c4 < 4; ++c4) {
+                    for (int c4 = 0; c4 < CH / 4; ++c4) {
                         const int4 at = reinterpret_cast<const int4 *>(rowoff + col0 + c0)[c4];
                         const int off[4] = {at.x, at.y, at.z, at.w};
 #pragma unroll
@@ -778,6 +806,7 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
                 uC = CL[ub];
                 if (NQ == 1 && lu > 0) cut_queries(ti, lu);
                 if (p.mask) {
+#pragma unroll 1
                     for (int k = ell; k < p.N; k += 128) umask[k] = __ldg(p.mask + (size_t)ub * p.N + k);
                     if (ok) ok = wg_sync();
                 }
@@ -804,102 +833,120 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
             if (ok && __any_sync(0xffffffffu, newk >= 0)) {
                 const int ibase = (uhr % p.RC) * P.Nc;
 #pragma unroll 1
-                for (int c0 = 0; c0 < CW; c0 += 16) {
-                    float x[16];
-                    tmem_ld16(saddr + c0, x);
+                for (int c0 = 0; c0 < CW; c0 += CH) {
+                    float x[CH];
+                    tmem_load<CH>(saddr + c0, x);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) {
+                    for (int c = 0; c < CH; ++c) {
                         // columns past the unit's rows: any answer will do
                         const int i = min(ibase + rowi[col0 + c0 + c], p.N - 1);
                         const bool bit = p.mask ? (umask[i] >> (newk & 63) & 1ull) != 0 : newk <= i;
                         if (newk >= 0 && !(bit && key < uC)) x[c] = -INFINITY;
                     }
-                    tmem_st16(saddr + c0, x);
+                    tmem_store<CH>(saddr + c0, x);
                 }
                 tmem_wait_st();
             }
 
             // x = s * qs is the exponent (log2 units, without the maximum); the
             // running maximum is of x + log2(V's scale), the weight that enters the
-            // product with V. It is raised only when one passes it by
-            // 2^RESCALE_LOG2. That is rare after a unit's first tile, so the tile's
+            // product with V. It is raised only when one passes it by 2^8
+            // (P_MAX). That is rare after a unit's first tile, so the tile's
             // weights are made against the maxima there are, and only then does the
             // warpgroup vote; if one was too large the maxima are raised and the tile
-            // is done again. A weight past the bound counts as the bound until then, so
-            // that its part of the row sum can be taken out again.
+            // is done again, its weights taken out of the row sums first.
             const int pb = lt % PB;
-            const float bound = RESCALE_LOG2 - lv;
-            uint8_t *pdst = p_buf + pb * L.p_bytes + (col0 / 16) * GROUP + ell * 16;
+            uint8_t *pdst = p_buf + pb * L.p_bytes + ell * 16;
+            auto p_at = [&](int c0) { return (col0 + c0) / 16 * GROUP + (col0 + c0) % 16; };
             if (lt >= PB && ok) ok = wait_w(&o_full[pb], ((lt - PB) / PB) & 1);  // P is free
             const bool fresh = first;
             bool raise = first, leave = false;
             while (true) {
                 if (!raise) {
-                    float top = -INFINITY;
+                    __half2 top2 = __float2half2_rn(0.f);
                     if (ok) {
 #pragma unroll 1
-                        for (int c0 = 0; c0 < CW; c0 += 16) {
-                            float x[16], l[16];
-                            tmem_ld16(saddr + c0, x);
-                            if (fresh) {
-#pragma unroll
-                                for (int c = 0; c < 16; ++c) l[c] = 0.f;
-                            } else {
-                                tmem_ld16(tm_l + c0, l);
-                            }
+                        for (int c0 = 0; c0 < CW; c0 += CH) {
+                            float x[CH], l[CH];
+                            tmem_load<CH>(saddr + c0, x);
+                            tmem_load<CH>(tm_l + c0, l);
                             tmem_wait_ld();
-                            uint32_t piece[3][4];
+                            // in phases over the chunk, so that no value waits for the one before
+                            uint64_t w[CH / 2];
+                            uint32_t h[CH / 2], piece[3][CH / 4];
 #pragma unroll
-                            for (int c4 = 0; c4 < 4; ++c4) {
+                            for (int c4 = 0; c4 < CH / 4; ++c4) {
                                 const ulonglong2 q4 = reinterpret_cast<const ulonglong2 *>(qs + c0)[c4];
                                 const ulonglong2 m4 = reinterpret_cast<const ulonglong2 *>(nm + c0)[c4];
-                                uint32_t h[2];
-#pragma unroll
-                                for (int i = 0; i < 2; ++i) {
-                                    const int c = c4 * 4 + 2 * i;
-                                    float a, b;
-                                    unpack2(fma2(mul2(pack2(x[c], x[c + 1]), ksc), i ? q4.y : q4.x, i ? m4.y : m4.x), a, b);
-                                    top = fmaxf(fmaxf(top, a), b);
-                                    const uint64_t w = pack2(ex2_approx(fmin_nan(a, bound)), ex2_approx(fmin_nan(b, bound)));
-                                    unpack2(add2(pack2(l[c], l[c + 1]), w), l[c], l[c + 1]);
-                                    unpack2(mul2(w, vsc), a, b);
-                                    const __half2 hh = __floats2half2_rn(a, b);
-                                    h[i] = *reinterpret_cast<const uint32_t *>(&hh);
-                                }
-                                piece[0][c4] = cut_piece(h, false);
-                                piece[1][c4] = cut_piece(h, false);
-                                piece[2][c4] = cut_piece(h, true);
+                                w[2 * c4] = fma2(mul2(pack2(x[c4 * 4], x[c4 * 4 + 1]), ksc), q4.x, m4.x);
+                                w[2 * c4 + 1] = fma2(mul2(pack2(x[c4 * 4 + 2], x[c4 * 4 + 3]), ksc), q4.y, m4.y);
                             }
-                            tmem_st16(tm_l + c0, l);
+#pragma unroll
+                            for (int i = 0; i < CH / 2; ++i) {
+                                float a, b;
+                                unpack2(w[i], a, b);
+                                w[i] = pack2(ex2_approx(a), ex2_approx(b));
+                            }
+#pragma unroll
+                            for (int i = 0; i < CH / 2; ++i) {
+                                float a, b;
+                                unpack2(add2(pack2(l[2 * i], l[2 * i + 1]), w[i]), l[2 * i], l[2 * i + 1]);
+                                unpack2(mul2(w[i], vsc), a, b);
+                                const __half2 hh = __floats2half2_rn(a, b);
+                                h[i] = *reinterpret_cast<const uint32_t *>(&hh);
+                            }
+                            {
+                                __half2 t[CH / 2];
+#pragma unroll
+                                for (int i = 0; i < CH / 2; ++i) t[i] = *reinterpret_cast<const __half2 *>(&h[i]);
+#pragma unroll
+                                for (int o = CH / 4; o > 0; o >>= 1)
+#pragma unroll
+                                    for (int i = 0; i < o; ++i) t[i] = __hmax2(t[i], t[i + o]);
+                                top2 = __hmax2(top2, t[0]);
+                            }
 #pragma unroll
                             for (int j = 0; j < 3; ++j)
-                                *reinterpret_cast<uint4 *>(pdst + (j * (RP / 16) + c0 / 16) * GROUP) =
-                                    make_uint4(piece[j][0], piece[j][1], piece[j][2], piece[j][3]);
+#pragma unroll
+                                for (int c4 = 0; c4 < CH / 4; ++c4) piece[j][c4] = cut_piece(h + 2 * c4, j == 2);
+                            tmem_store<CH>(tm_l + c0, l);
+#pragma unroll
+                            for (int j = 0; j < 3; ++j)
+                                if constexpr (CH == 16)
+                                    *reinterpret_cast<uint4 *>(pdst + (j * (RP / 16) * GROUP + p_at(c0))) =
+                                        make_uint4(piece[j][0], piece[j][1], piece[j][2], piece[j][3]);
+                                else
+                                    *reinterpret_cast<uint2 *>(pdst + (j * (RP / 16) * GROUP + p_at(c0))) =
+                                        make_uint2(piece[j][0], piece[j][1]);
                         }
                         tmem_wait_st();
                     }
-                    raise = wg_any(1 + wg, !ok || top > bound);
+                    raise = wg_any(1 + wg, !ok || !__hble2(top2, __float2half2_rn(P_MAX)));
                     if (!raise) break;
                 }
                 if ((leave = wg_any(1 + wg, !ok))) break;
                 // tile column maxima over the 128 keys; this tile's weights out of the row sums
 #pragma unroll 1
-                for (int c0 = 0; c0 < CW; c0 += 16) {
-                    float y[16], l[16], mine = 0.f;
-                    tmem_ld16(saddr + c0, y);
-                    if (!fresh) tmem_ld16(tm_l + c0, l);
+                for (int c0 = 0; c0 < CW; c0 += CH) {
+                    float y[CH], l[CH], mine = 0.f;
+                    tmem_load<CH>(saddr + c0, y);
+                    if (!fresh) tmem_load<CH>(tm_l + c0, l);
+                    else
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) l[c] = 0.f;
                     tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) {
+                    for (int c = 0; c < CH; ++c) {
                         const float e = y[c] * ks1;
                         float m;
                         asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(fmaf(e, qs[c0 + c], lv)));
                         if (lane == c) mine = m;
-                        if (!fresh) l[c] -= ex2_approx(fmin_nan(fmaf(e, qs[c0 + c], nm[c0 + c]), bound));
+                        // a sum that overflowed held nothing that counts beside the weight that made it so
+                        if (!fresh) l[c] = l[c] == INFINITY ? 0.f : l[c] - ex2_approx(fmaf(e, qs[c0 + c], nm[c0 + c]));
                     }
-                    if (!fresh) tmem_st16(tm_l + c0, l);
-                    if (lane < 16) red[wiw * RP + c0 + lane] = mine;
+                    tmem_store<CH>(tm_l + c0, l);
+                    if (lane < CH) red[wiw * RP + c0 + lane] = mine;
                 }
                 tmem_wait_st();
                 ok = wg_sync();
@@ -917,15 +964,15 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
                     tc_fence_after();
                     if (ok) {
 #pragma unroll 1
-                        for (int i = 0; i < CW / 16 * (ACC + 1); ++i) {
-                            const int c0 = i / (ACC + 1) * 16, k = i % (ACC + 1);
+                        for (int i = 0; i < CW / CH * (ACC + 1); ++i) {
+                            const int c0 = i / (ACC + 1) * CH, k = i % (ACC + 1);
                             const uint32_t at = k == ACC ? tm_l + c0 : tm_o + k * RP + c0;
-                            float o[16];
-                            tmem_ld16(at, o);
+                            float o[CH];
+                            tmem_load<CH>(at, o);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int c = 0; c < 16; ++c) o[c] *= as[c0 + c];
-                            tmem_st16(at, o);
+                            for (int c = 0; c < CH; ++c) o[c] *= as[c0 + c];
+                            tmem_store<CH>(at, o);
                         }
                         tmem_wait_st();
                     }

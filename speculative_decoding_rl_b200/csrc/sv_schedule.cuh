@@ -45,6 +45,7 @@ SV_DEV void tile_prefix(const AttnParams &p, int *TP, int *scratch, int *CL = nu
     const int per = (p.B + nt - 1) / nt;
     const int s0 = min(tid * per, p.B), s1 = min(s0 + per, p.B);
     int local = 0;
+#pragma unroll 1
     for (int b = s0; b < s1; ++b) {
         local += seq_slots(p, b);
         if (CL) CL[b] = p.ctx_lens[b];
@@ -59,8 +60,10 @@ SV_DEV void tile_prefix(const AttnParams &p, int *TP, int *scratch, int *CL = nu
     if (lane == 31) scratch[warp] = incl;
     __syncthreads();
     int wpre = 0;
+#pragma unroll 1
     for (int w = 0; w < warp; ++w) wpre += scratch[w];
     int run = wpre + incl - local;
+#pragma unroll 1
     for (int b = s0; b < s1; ++b) {
         TP[b] = run;
         run += seq_slots(p, b);
@@ -77,6 +80,7 @@ SV_DEV int schedule_width(const AttnParams &p, int total) {
 // Schedule position t -> sequence b (largest b with ups*TP[b] <= t).
 SV_DEV int tile_seq(const int *TP, int B, int ups, int t) {
     int lo = 0, hi = B;
+#pragma unroll 1
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (ups * TP[mid] <= t) lo = mid; else hi = mid;
@@ -97,6 +101,7 @@ SV_DEV void next_tile(TileInfo &ti, const int *TP, int B, int ups) {
     ti.j = 0;
     if (++ti.hr < ups) return;
     ti.hr = 0;
+#pragma unroll 1
     do {
         ++ti.b;
         ti.Tb = ti.b < B ? real_tiles(TP[ti.b + 1] - TP[ti.b]) : 1;
@@ -121,6 +126,7 @@ SV_DEV TileInfo cta_tiles(const int *TP, int B, int ups, int v0, int v1, int *nt
     }
     TileInfo w = ti;
     int n = 0;
+#pragma unroll 1
     while (w.b < B) {
         const int pos = ups * TP[w.b] + w.hr * (w.Tb + UNIT_COST) + w.j;
         if (pos >= v1) break;
