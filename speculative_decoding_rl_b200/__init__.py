@@ -20,8 +20,9 @@ __all__ = [
     "sv_accept_workspace_size",
     "SvCascadeDesc", "make_cascade_desc", "sv_cascade_attention_workspace_size", "sv_cascade_verify_attention",
     "sv_kv_commit", "make_kv_layers", "SvRopeDesc", "SvNewRows", "SvKVQ8", "make_rope_desc", "make_new_rows",
-    "make_kv_q8", "sv_kv_append", "sv_kv_append_q8", "sv_verify_attention_q8_workspace_size",
-    "sv_verify_attention_q8", "sv_kv_commit_q8", "make_kv_q8_layers", "SdController", "SvCtlConfig", "SvHistoryDesc", "sv_history_draft",
+    "make_kv_q8", "PreparedCall", "sv_kv_append", "sv_kv_append_q8", "sv_verify_attention_q8_workspace_size",
+    "sv_verify_attention_q8", "sv_kv_commit_q8", "make_kv_q8_layers", "SdController", "SvCtlConfig", "SvHistoryDesc",
+    "sv_history_draft",
     "sv_status_string", "sv_last_error", "sv_version", "library_path",
     "sv_testing_philox4x32_10", "sv_testing_verify_attention_stalled", "SV_FLAG_TIMEOUT",
     "SV_FLAG_NONFINITE", "SV_FLAG_BAD_CONTEXT", "SV_FLAG_BAD_TOKEN", "SV_FLAG_BAD_BLOCK",
@@ -377,6 +378,51 @@ def make_kv_q8_layers(layers) -> C.Array:
     arr = (SvKVQ8 * len(each))(*each)
     arr._keep = each
     return arr
+
+
+class PreparedCall:
+    """An entry point with all its arguments but the stream bound once: a call costs one foreign call.
+
+    Arguments are passed as to the entry point of that name; they and the tensors in ``beside`` are kept alive and
+    must be on one CUDA device. A call runs on that device's current stream unless given one."""
+
+    def __init__(self, entry: str, *args, beside=()):
+        import torch
+        tensors = [x for x in (*args, *beside) if isinstance(x, torch.Tensor)]
+        devices = {x.device for x in tensors}
+        if len(devices) != 1 or next(iter(devices)).type != "cuda":
+            raise ValueError(f"the tensors of a call must be on one CUDA device, got {sorted(map(str, devices))}")
+        self._device = next(iter(devices)).index
+        self._keep = (args, tuple(beside))
+        self._fn = getattr(_L(), entry)
+        bound = []
+        for x in args:
+            if isinstance(x, C.Array):
+                bound.append(x)
+            elif isinstance(x, C.Structure):
+                bound.append(C.byref(x))
+            elif x is None or isinstance(x, torch.Tensor):
+                bound.append(C.c_void_p(_ptr(x)))
+            else:
+                bound.append(x)
+        self._args = tuple(bound)
+        self._torch = torch
+        # the stream's address without a Stream object around it, where torch offers it
+        self._raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+    def __call__(self, stream=None) -> None:
+        if stream is None:
+            stream = self._raw(self._device)
+        elif not isinstance(stream, int):
+            stream = stream.cuda_stream
+        if self._torch.cuda.current_device() == self._device:
+            st = self._fn(*self._args, stream)
+        else:
+            with self._torch.cuda.device(self._device):
+                st = self._fn(*self._args, stream)
+        if st:
+            _check(st)
 
 
 def sv_kv_append(desc: SvAttnDesc, rope: SvRopeDesc, rows: SvNewRows, kv: SvKVLayer, block_table, ctx_lens, q_out,

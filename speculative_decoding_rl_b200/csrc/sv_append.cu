@@ -7,13 +7,13 @@
 // are rounded one by one (no contraction), so the result is the formula's in
 // fp32, bit for bit, whatever the compiler does.
 //
-// The rows of a sequence are taken page by page of the cache: grid (pages a
-// sequence's rows can touch, sequences, parts). In the bf16 call every part is
-// one row of the page: all of its heads, 8 entries (16 bytes) per thread, a
-// thread keeping its cosines and sines for the heads it takes. In the 8-bit
-// call the first parts are the page's K and V, one warp to each (KV head, K or
-// V), since a page's scale is the maximum over its rows; the others rotate q as
-// the bf16 call does.
+// q, and K and V of the bf16 call: a CTA takes one row (or a few, where a row has
+// few heads), a thread 8 entries (16 bytes) of up to AP_BATCH heads at a time and
+// their cosines and sines once. K and V of the 8-bit call: a page's scale is the
+// maximum over its rows, so two warps take the page of one KV head, K or V.
+// Little is computed; what bounds a call is memory when there are many rows, and
+// the chain of loads (length, then block id and positions, then cosines and
+// sines) when there are few, so the rows themselves are asked for first.
 #include "sv_page8.cuh"
 #include "sv_q8.h"
 
@@ -23,7 +23,7 @@ namespace {
 constexpr int AP_THREADS = 256;
 constexpr int AP_WARPS = AP_THREADS / 32;
 
-// What a CTA needs to know of its sequence and page.
+// What a CTA needs to know of its sequence.
 struct Seq {
     int C, n, start;  // context length, new rows, cache position of the first
     bool ok;
@@ -60,18 +60,26 @@ SV_DEV void write_status(const AppendParams &p, const Seq &s, int b) {
         p.status[b] = (!s.ok || bad_pos ? SV_FLAG_BAD_CONTEXT : 0) | (bad_blk ? SV_FLAG_BAD_BLOCK : 0);
 }
 
-// New rows [i0, i1) of sequence b on `page` and its block id (-1: the page is
-// skipped, for a bad id or a bad position among those rows). Warp by warp, no
-// barrier; every lane of the warp takes part.
-SV_DEV int check_page(const AppendParams &p, const Seq &s, int b, int page, int *i0, int *i1) {
-    const int lane = threadIdx.x & 31;
-    *i0 = max(page * PAGE, s.start) - s.start;
-    *i1 = min(page * PAGE + PAGE, s.C) - s.start;
-    const int blk = p.block_table[(size_t)b * p.max_blocks + page];
-    const int i = *i0 + lane;
-    const bool bad = lane < PAGE && i < *i1 && bad_position(p, row_position(p, s, b, i));
-    return __any_sync(0xffffffffu, bad) || blk < 0 || blk >= p.num_blocks ? -1 : blk;
-}
+// A page of a sequence that gets new rows: its new rows [i0, i1), its block id
+// and, in lanes 0..15 of every warp, its new rows' positions. Loads only; ok()
+// looks at them, so that a caller can send its own loads in between.
+struct PageRows {
+    int page, i0, i1, blk, pos;
+
+    SV_DEV PageRows(const AppendParams &p, const Seq &s, int b, int page_) : page(page_) {
+        const int lane = threadIdx.x & 31;
+        i0 = max(page * PAGE, s.start) - s.start;
+        i1 = min(page * PAGE + PAGE, s.C) - s.start;
+        blk = p.block_table[(size_t)b * p.max_blocks + page];
+        pos = lane < PAGE && i0 + lane < i1 ? row_position(p, s, b, i0 + lane) : 0;
+    }
+    // Every lane of the warp takes part; false: the page is skipped.
+    SV_DEV bool ok(const AppendParams &p) const {
+        const int lane = threadIdx.x & 31;
+        const bool bad = lane < PAGE && i0 + lane < i1 && bad_position(p, pos);
+        return !__any_sync(0xffffffffu, bad) && blk >= 0 && blk < p.num_blocks;
+    }
+};
 
 // The cosines and sines that 8 entries [8c, 8c + 8) of a head turn by.
 struct Turn {
@@ -137,138 +145,212 @@ SV_DEV void turn8(const AppendParams &p, const Turn &t, int c, float *x, const f
 // Chunk that chunk c pairs with in the half layout.
 SV_DEV int pair_chunk(const AppendParams &p, int c) { return 16 * c < p.R ? c + p.R / 16 : c - p.R / 16; }
 
-// Heads [0, heads) of row i of sequence b, a thread per 8 entries: q to q_out,
-// and (KV) k and v to their page of the bf16 cache.
+constexpr int AP_BATCH = 4;
+
+// Heads of row i of sequence b by `group` threads (whole warps): q to q_out, and
+// (KV) k and v to their page of the bf16 cache.
 template <bool KV>
-SV_DEV void rotate_row(const AppendParams &p, const Seq &s, int b, int i, int blk) {
+SV_DEV void rotate_row(const AppendParams &p, int b, int i, int tid, int group) {
     const int chunks = p.D / 8;
-    const int lanes = AP_THREADS / chunks;  // heads in flight
-    const int c = threadIdx.x % chunks, h0 = threadIdx.x / chunks;
-    if (h0 >= lanes) return;  // D / 8 does not divide the CTA
-    Turn t;
-    t.on = false;
-    if (p.R > 0) t.load(p, row_position(p, s, b, i), c);
-    const bool pairs = t.on && !p.interleaved;
+    const int lanes = group / chunks;  // heads in flight
+    const int c = tid % chunks, h0 = tid / chunks;
     const size_t row = (size_t)b * p.N + i;
     const int hq = p.q ? p.Hq : 0;
-    const int heads = hq + (KV ? 2 * p.Hkv : 0);
+    // D / 8 need not divide the group; rows past new_lens are not read
+    const int n = p.new_lens ? p.new_lens[b] : p.N;
+    const int heads = h0 < lanes && i < n && i < p.N ? hq + (KV ? 2 * p.Hkv : 0) : 0;
+    auto source = [&](int h) {
+        const int hk = h >= hq + p.Hkv ? h - hq - p.Hkv : h - hq;
+        const uint16_t *src = h < hq ? p.q + row * p.q_stride + (size_t)h * p.D
+                                     : (h >= hq + p.Hkv ? p.v : p.k) + row * p.kv_stride + (size_t)hk * p.D;
+        return reinterpret_cast<const uint4 *>(src);
+    };
+    uint4 own[AP_BATCH];
+    auto fetch = [&](int h) {
+#pragma unroll
+        for (int k = 0; k < AP_BATCH; ++k)
+            if (h + k * lanes < heads) own[k] = __ldg(source(h + k * lanes) + c);
+    };
+    fetch(h0);
+    const Seq s = read_seq(p, b);
+    if (!s.ok || i >= s.n) return;
+    const PageRows pr(p, s, b, (s.start + i) / PAGE);
+    const int t = __shfl_sync(0xffffffffu, pr.pos, i - pr.i0);
+    if (!pr.ok(p)) return;
+    Turn turn;
+    turn.on = false;
+    if (p.R > 0) turn.load(p, t, c);
+    const bool pairs = !p.interleaved && p.R > 0;  // with the chunk pair_chunk, for the chunks that turn
+    const bool near = 32 % chunks == 0;            // which a lane of the warp holds
+    const int pc = turn.on ? pair_chunk(p, c) : c, mate = (int)(threadIdx.x & 31) - c + pc;
     const int at = (s.start + i) % PAGE;
-#pragma unroll 4
-    for (int h = h0; h < heads; h += lanes) {
-        const bool is_q = h < hq, is_v = h >= hq + p.Hkv;
-        const int hk = is_v ? h - hq - p.Hkv : h - hq;
-        const uint16_t *src = is_q ? p.q + row * p.q_stride + (size_t)h * p.D
-                                   : (is_v ? p.v : p.k) + row * p.kv_stride + (size_t)hk * p.D;
-        uint4 own = __ldg(reinterpret_cast<const uint4 *>(src) + c);
-        if (t.on && !is_v) {
-            float x[8], o[8];
-            unpack8(own, x);
-            if (pairs) unpack8(__ldg(reinterpret_cast<const uint4 *>(src) + pair_chunk(p, c)), o);
-            turn8(p, t, c, x, o);
-            own = pack8(x);
+    const int rounds = (hq + (KV ? 2 * p.Hkv : 0) + AP_BATCH * lanes - 1) / (AP_BATCH * lanes);
+#pragma unroll 1
+    for (int r = 0; r < rounds; ++r) {
+        const int h = h0 + r * AP_BATCH * lanes;
+        if (r) fetch(h);
+#pragma unroll
+        for (int k = 0; k < AP_BATCH; ++k) {
+            const int hh = h + k * lanes;
+            const bool is_q = hh < hq, is_v = hh >= hq + p.Hkv;
+            uint4 m = own[k];
+            if (pairs) {
+                if (near) {
+                    m.x = __shfl_sync(0xffffffffu, own[k].x, mate);
+                    m.y = __shfl_sync(0xffffffffu, own[k].y, mate);
+                    m.z = __shfl_sync(0xffffffffu, own[k].z, mate);
+                    m.w = __shfl_sync(0xffffffffu, own[k].w, mate);
+                } else if (hh < heads) {
+                    m = __ldg(source(hh) + pc);
+                }
+            }
+            if (hh >= heads) continue;
+            const int hk = is_v ? hh - hq - p.Hkv : hh - hq;
+            if (turn.on && !is_v) {
+                float x[8], o[8];
+                unpack8(own[k], x);
+                unpack8(m, o);
+                turn8(p, turn, c, x, o);
+                own[k] = pack8(x);
+            }
+            uint16_t *dst;
+            if (is_q) {
+                dst = p.q_out + (row * p.Hq + hh) * p.D;
+            } else {
+                uint16_t *pool = static_cast<uint16_t *>(is_v ? p.v_pool : p.k_pool);
+                dst = pool + (((size_t)pr.blk * p.Hkv + hk) * PAGE + at) * p.D;
+            }
+            reinterpret_cast<uint4 *>(dst)[c] = own[k];
         }
-        uint16_t *dst;
-        if (is_q) {
-            dst = p.q_out + (row * p.Hq + h) * p.D;
-        } else {
-            uint16_t *pool = static_cast<uint16_t *>(is_v ? p.v_pool : p.k_pool);
-            dst = pool + (((size_t)blk * p.Hkv + hk) * PAGE + at) * p.D;
-        }
-        reinterpret_cast<uint4 *>(dst)[c] = own;
     }
 }
 
-__global__ void __launch_bounds__(AP_THREADS) append_kernel(const __grid_constant__ AppendParams p) {
-    const int b = blockIdx.y;
-    const Seq s = read_seq(p, b);
-    if (p.status && blockIdx.x == 0 && blockIdx.z == 0) write_status(p, s, b);
-    const int page = s.start / PAGE + blockIdx.x;
-    if (!s.ok || s.n == 0 || page * PAGE >= s.C) return;
-    int i0, i1;
-    const int blk = check_page(p, s, b, page, &i0, &i1);
-    const int row = i0 + (int)blockIdx.z;  // part z is the z-th new row of the page
-    if (blk >= 0 && row < i1) rotate_row<true>(p, s, b, row, blk);
+// Rows a CTA takes: as many as leave a thread no more than one batch of a row's
+// heads, in whole warps.
+int rows_per_cta(const AppendParams &p, bool kv) {
+    const int items = ((p.q ? p.Hq : 0) + (kv ? 2 * p.Hkv : 0)) * (p.D / 8);
+    int rows = 1;
+    while (rows < AP_WARPS && AP_THREADS / (2 * rows) * AP_BATCH >= items && AP_THREADS / (2 * rows) >= p.D / 8) rows *= 2;
+    return rows;
 }
 
-// One page of one KV head, K or V, by a warp.
+__global__ void __launch_bounds__(AP_THREADS, 4) append_kernel(const __grid_constant__ AppendParams p, int rows) {
+    const int b = blockIdx.y, group = AP_THREADS / rows, sub = threadIdx.x / group;
+    if (p.status && blockIdx.x == 0) write_status(p, read_seq(p, b), b);
+    rotate_row<true>(p, b, blockIdx.x * rows + sub, threadIdx.x - sub * group, group);
+}
+
+// One page of one KV head, K or V, by two warps, each half of its rows; the
+// whole CTA comes here for one page. tops: a float per warp.
 template <int D>
-SV_DEV void append_page(const AppendParams &p, const Seq &s, int b, int page, int blk, int hk, bool is_v, int lane) {
-    uint8_t *dst = static_cast<uint8_t *>(is_v ? p.v_pool : p.k_pool) + ((size_t)blk * p.Hkv + hk) * PAGE * D;
-    float *scale = p.scales + ((size_t)blk * p.Hkv + hk) * 2 + (is_v ? 1 : 0);
-    const float old_scale = page * PAGE < s.start ? *scale : 0.f;
-    const uint16_t *src = is_v ? p.v : p.k;
-    const int c = Page8<D>::col(lane) / 8;
-    const bool pairs = !is_v && !p.interleaved && 8 * c < p.R;
+SV_DEV void append_page(const AppendParams &p, int b, int index, int job, bool has_job, int warp, int lane, float *tops) {
+    using Pg = Page8<D>;
+    constexpr int NS = Pg::STEPS / 2;
+    const Seq s = read_seq(p, b);
+    const int page = s.start / PAGE + index;
+    if (!s.ok || s.n == 0 || page * PAGE >= s.C) return;
+    const int hk = job >> 1, S0 = (warp & 1) * NS;
+    const bool is_v = job & 1;
+    const uint16_t *src = (is_v ? p.v : p.k) + (size_t)b * p.N * p.kv_stride + (size_t)hk * D;
+    const int c = Pg::col(lane) / 8;
+    const bool turns = !is_v && 8 * c < p.R, pairs = turns && !p.interleaved;
     // the lane of this lane's row that holds the paired chunk
     const int mate = lane - c + (pairs ? pair_chunk(p, c) : c);
-    Page8<D> pg;
+    const int first = page * PAGE - s.start;  // the new row on the page's row 0, if there is one
+    uint4 own[NS];
 #pragma unroll
-    for (int st = 0; st < Page8<D>::STEPS; ++st) {
-        const int r = Page8<D>::row(st, lane);
-        const int t = page * PAGE + r, i = t - s.start;
-        uint4 own = make_uint4(0, 0, 0, 0);
-        const bool fresh = i >= 0 && i < s.n;
-        if (fresh)
-            own = __ldg(reinterpret_cast<const uint4 *>(src + ((size_t)b * p.N + i) * p.kv_stride + (size_t)hk * D) + c);
-        else if (i < 0)
-            *reinterpret_cast<uint2 *>(&own) = *reinterpret_cast<const uint2 *>(dst + r * D + 8 * c);
-        float o[8];
-        {
-            uint4 m;
-            m.x = __shfl_sync(0xffffffffu, own.x, mate);
-            m.y = __shfl_sync(0xffffffffu, own.y, mate);
-            m.z = __shfl_sync(0xffffffffu, own.z, mate);
-            m.w = __shfl_sync(0xffffffffu, own.w, mate);
-            unpack8(m, o);
-        }
-        if (i < 0) {
-            pg.set(st, make_uint2(own.x, own.y), old_scale);
-        } else {
-            unpack8(own, pg.val[st]);
-            if (fresh && !is_v && 8 * c < p.R) {
-                Turn tn;
-                tn.load(p, row_position(p, s, b, i), c);
-                turn8(p, tn, c, pg.val[st], o);
+    for (int st = 0; st < NS; ++st) {
+        const int i = first + Pg::row(S0 + st, lane);
+        own[st] = make_uint4(0, 0, 0, 0);
+        if (has_job && i >= 0 && i < s.n) own[st] = __ldg(reinterpret_cast<const uint4 *>(src + i * p.kv_stride) + c);
+    }
+    const PageRows pr(p, s, b, page);
+    if (!pr.ok(p)) return;  // the same for every warp of the CTA
+    uint8_t *dst = static_cast<uint8_t *>(is_v ? p.v_pool : p.k_pool) + ((size_t)pr.blk * p.Hkv + hk) * PAGE * D;
+    float *scale = p.scales + ((size_t)pr.blk * p.Hkv + hk) * 2 + (is_v ? 1 : 0);
+    float val[NS][8];
+    if (has_job && first < 0) {  // rows that are there already
+        const float old_scale = *scale;
+#pragma unroll
+        for (int st = 0; st < NS; ++st) {
+            const int r = Pg::row(S0 + st, lane);
+            if (first + r < 0) {
+                const uint2 bytes = *reinterpret_cast<const uint2 *>(dst + r * D + 8 * c);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) unpack_e4m3(bytes, j, old_scale, val[st][2 * j], val[st][2 * j + 1]);
             }
         }
     }
-    pg.store(dst, scale, min(PAGE, s.C - page * PAGE), lane);
+#pragma unroll
+    for (int st = 0; st < NS; ++st) {
+        const int i = first + Pg::row(S0 + st, lane);
+        float o[8];
+        if (!is_v && !p.interleaved) {
+            uint4 m;
+            m.x = __shfl_sync(0xffffffffu, own[st].x, mate);
+            m.y = __shfl_sync(0xffffffffu, own[st].y, mate);
+            m.z = __shfl_sync(0xffffffffu, own[st].z, mate);
+            m.w = __shfl_sync(0xffffffffu, own[st].w, mate);
+            unpack8(m, o);
+        }
+        const int t = __shfl_sync(0xffffffffu, pr.pos, (i - pr.i0) & 31);
+        if (i >= 0) {
+            unpack8(own[st], val[st]);
+            if (turns && i < s.n) {
+                Turn tn;
+                tn.load(p, t, c);
+                turn8(p, tn, c, val[st], o);
+            }
+        }
+    }
+    const int kept = min(PAGE, s.C - page * PAGE);
+    auto get = [&](int st, int j, float &x, float &y) {
+        x = val[st][2 * j];
+        y = val[st][2 * j + 1];
+    };
+    const float top = warp_max(has_job ? Pg::template top<NS>(S0, kept, lane, get) : 0.f);
+    if (lane == 0) tops[warp] = top;
+    __syncthreads();  // both halves have read the page and its scale before one writes
+    if (!has_job) return;
+    const int e = page8_exponent(fmaxf(tops[warp], tops[warp ^ 1]));
+    if (lane == 0 && !(warp & 1)) *scale = exp2_int(e);
+    Pg::template write<NS>(dst, e, S0, kept, lane, get);
 }
 
+// Grid: (pages a sequence's rows can touch x kv_parts, then its rows; sequences).
 template <int D>
-__global__ void __launch_bounds__(AP_THREADS) append_q8_kernel(const __grid_constant__ AppendParams p, int kv_parts) {
-    const int b = blockIdx.y;
-    const Seq s = read_seq(p, b);
-    if (p.status && blockIdx.x == 0 && blockIdx.z == 0) write_status(p, s, b);
-    const int page = s.start / PAGE + blockIdx.x;
-    if (!s.ok || s.n == 0 || page * PAGE >= s.C) return;
-    int i0, i1;
-    const int blk = check_page(p, s, b, page, &i0, &i1);
-    if (blk < 0) return;
-    if ((int)blockIdx.z < kv_parts) {
-        const int job = blockIdx.z * AP_WARPS + (threadIdx.x >> 5);
-        if (job < 2 * p.Hkv) append_page<D>(p, s, b, page, blk, job >> 1, job & 1, threadIdx.x & 31);
-        return;
+__global__ void __launch_bounds__(AP_THREADS, 3) append_q8_kernel(const __grid_constant__ AppendParams p, int pages,
+                                                                  int kv_parts, int rows) {
+    __shared__ float tops[AP_WARPS];
+    const int b = blockIdx.y, warp = threadIdx.x >> 5;
+    if (p.status && blockIdx.x == 0) write_status(p, read_seq(p, b), b);
+    const int x = blockIdx.x - pages * kv_parts;
+    if (x < 0) {
+        const int index = blockIdx.x / kv_parts, part = blockIdx.x - index * kv_parts;
+        const int job = part * (AP_WARPS / 2) + (warp >> 1);
+        append_page<D>(p, b, index, job, job < 2 * p.Hkv, warp, threadIdx.x & 31, tops);
+    } else {
+        const int group = AP_THREADS / rows, sub = threadIdx.x / group;
+        rotate_row<false>(p, b, x * rows + sub, threadIdx.x - sub * group, group);
     }
-    const int row = i0 + (int)blockIdx.z - kv_parts;
-    if (row < i1) rotate_row<false>(p, s, b, row, 0);
 }
 
 }  // namespace
 
 cudaError_t launch_append(const AppendParams &p, bool q8, cudaStream_t stream) {
-    // pages that N consecutive positions can touch, and new rows on one of them
-    const unsigned pages = (unsigned)((p.N + PAGE - 2) / PAGE + 1), rows = (unsigned)(p.N < PAGE ? p.N : PAGE);
+    const int rows = rows_per_cta(p, !q8);
+    const unsigned row_ctas = (unsigned)((p.N + rows - 1) / rows);
     if (!q8) {
-        append_kernel<<<dim3(pages, (unsigned)p.B, rows), AP_THREADS, 0, stream>>>(p);
+        append_kernel<<<dim3(row_ctas, (unsigned)p.B), AP_THREADS, 0, stream>>>(p, rows);
         return cudaGetLastError();
     }
-    const int kv_parts = (2 * p.Hkv + AP_WARPS - 1) / AP_WARPS;
-    const dim3 grid(pages, (unsigned)p.B, (unsigned)kv_parts + (p.q ? rows : 0u));
+    const int pages = (p.N + PAGE - 2) / PAGE + 1;  // that N consecutive positions can touch
+    const int kv_parts = (2 * p.Hkv + AP_WARPS / 2 - 1) / (AP_WARPS / 2);
+    const dim3 grid((unsigned)pages * kv_parts + (p.q ? row_ctas : 0u), (unsigned)p.B);
     if (p.D == 128)
-        append_q8_kernel<128><<<grid, AP_THREADS, 0, stream>>>(p, kv_parts);
+        append_q8_kernel<128><<<grid, AP_THREADS, 0, stream>>>(p, pages, kv_parts, rows);
     else
-        append_q8_kernel<64><<<grid, AP_THREADS, 0, stream>>>(p, kv_parts);
+        append_q8_kernel<64><<<grid, AP_THREADS, 0, stream>>>(p, pages, kv_parts, rows);
     return cudaGetLastError();
 }
 

@@ -4,79 +4,120 @@
 //
 // A row that moves to another page comes under another scale, so a page that
 // receives a row is rebuilt: its kept rows, each from where it was, under the
-// smallest power of two that holds them. One CTA per (sequence, KV head,
-// layer); a warp for each page that can receive a row and K or V holds that
-// page's 16 rows in registers, and the CTA writes after every warp has read (a
-// destination can be another move's source).
+// smallest power of two that holds them. A job is K or V of one (sequence,
+// layer, KV head); a warp holds one page of it in registers and goes over the
+// pages in ascending order. Rows only move down (path[k] >= k + 1), so what a
+// page still has to give goes to itself or to a page before it, and no warp
+// waits for another.
+//
+// The call moves little; what bounds it is the chain of loads (lengths and
+// path, then block ids, then rows and scales) and the number of warps that run
+// through it. A warp therefore does all jobs it is given after one walk of the
+// first two steps, as many as make the grid fill the SMs about once.
 #include "sv_page8.cuh"
 #include "sv_q8.h"
 
 namespace sv {
 namespace {
 
+constexpr int CQ_WARPS = 8;
+
 template <int D>
-__global__ void __launch_bounds__(320) kv_commit_q8_kernel(const __grid_constant__ CommitQ8Launch P) {
-    const int b = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+__global__ void __launch_bounds__(32 * CQ_WARPS, 3) kv_commit_q8_kernel(const __grid_constant__ CommitQ8Launch P,
+                                                                     int stride) {
+    const int b = blockIdx.x, lane = threadIdx.x & 31;
+    const int first = blockIdx.y * CQ_WARPS + (threadIdx.x >> 5);
     const int N = P.N, C = P.ctx_lens[b], a = P.accept_len[b];
-    const int *tbl = P.block_table + (size_t)b * P.max_blocks;
+    // path[k] in lane k % 32
     const int *path = P.accept_path + (size_t)b * (N > 1 ? N - 1 : 1);
-    int f = 0;
-    if (C < N || C > P.max_blocks * PAGE) f |= SV_FLAG_BAD_CONTEXT;
-    if (!f)
-        for (int pg = (C - N) / PAGE; pg <= (C - 1) / PAGE; ++pg)
-            if (tbl[pg] < 0 || tbl[pg] >= P.num_blocks) { f |= SV_FLAG_BAD_BLOCK; break; }
-    int k0 = a;  // first accepted node that moves; all later ones move too
-    if (a < 0 || a > N - 1) {
-        f |= SV_FLAG_BAD_PATH;
-    } else {
-        for (int k = 0, prev = 0; k < a; ++k) {
-            const int node = path[k];
-            if (node < 1 || node > N - 1 || node <= prev) { f |= SV_FLAG_BAD_PATH; break; }
-            if (node != k + 1 && k0 == a) k0 = k;
-            prev = node;
-        }
+    const int n0 = lane < N - 1 ? path[lane] : 0, n1 = lane + 32 < N - 1 ? path[lane + 32] : 0;
+    auto node = [&](int k) {  // any k in [0, 64); all lanes take part
+        const int x = __shfl_sync(0xffffffffu, n0, k & 31), y = __shfl_sync(0xffffffffu, n1, k & 31);
+        return k < 32 ? x : y;
+    };
+    const int root = C - N;
+    int f = C < N || C > P.max_blocks * PAGE ? SV_FLAG_BAD_CONTEXT : 0;
+    // block ids of the pages that hold the new rows, lane by lane (N <= 64: at most 5)
+    const int page0 = f ? 0 : root / PAGE;
+    int blk = 0;
+    bool bad_blk = false;
+    if (!f && page0 + lane <= (C - 1) / PAGE) {
+        blk = P.block_table[(size_t)b * P.max_blocks + page0 + lane];
+        bad_blk = blk < 0 || blk >= P.num_blocks;
     }
-    if (h == 0 && blockIdx.z == 0 && tid == 0) {
+    if (__any_sync(0xffffffffu, bad_blk)) f |= SV_FLAG_BAD_BLOCK;
+    const bool len_ok = a >= 0 && a <= N - 1;
+    const int m0 = __shfl_up_sync(0xffffffffu, n0, 1), m1 = __shfl_up_sync(0xffffffffu, n1, 1);
+    const int top0 = __shfl_sync(0xffffffffu, n0, 31);
+    const int prev0 = lane ? m0 : 0, prev1 = lane ? m1 : top0;
+    const bool bad0 = lane < a && (n0 <= prev0 || n0 > N - 1), bad1 = lane + 32 < a && (n1 <= prev1 || n1 > N - 1);
+    if (!len_ok || __any_sync(0xffffffffu, bad0 || bad1)) f |= SV_FLAG_BAD_PATH;
+    if (first == 0 && lane == 0) {
         P.new_ctx[b] = f ? C : C - N + 1 + a;
         if (P.status) P.status[b] = f;
     }
-    if (f || k0 == a) return;
-
-    const sv_kv_q8 &layer = P.layer[blockIdx.z];
-    const int root = C - N, last = root + a;  // the last position kept
-    const int page = (root + 1 + k0) / PAGE + (warp >> 1);
-    const bool is_v = warp & 1, mine = page <= last / PAGE;
-    uint8_t *pool = static_cast<uint8_t *>(is_v ? layer.v_pool : layer.k_pool);
-    Page8<D> pg;
-    if (mine) {
+    if (f) return;
+    // first accepted node that moves; all later ones move too
+    const unsigned mv0 = __ballot_sync(0xffffffffu, lane < a && n0 != lane + 1);
+    const unsigned mv1 = __ballot_sync(0xffffffffu, lane + 32 < a && n1 != lane + 33);
+    if (!(mv0 | mv1)) return;
+    const int k0 = mv0 ? __ffs(mv0) - 1 : 31 + __ffs(mv1);
+    const int last = root + a;  // the last position kept
+    const int jobs = 2 * P.Hkv * P.L;
+    for (int page = (root + 1 + k0) / PAGE; page <= last / PAGE; ++page) {
+        // where the rows of this lane come from: page's index among the loaded ids and row
+        int from[Page8<D>::STEPS];
 #pragma unroll
         for (int st = 0; st < Page8<D>::STEPS; ++st) {
             const int t = page * PAGE + Page8<D>::row(st, lane);
-            if (t > last) continue;
-            const int src = t > root + k0 ? root + path[t - root - 1] : t;
-            const size_t at = (size_t)tbl[src / PAGE] * P.Hkv + h;
-            pg.set(st,
-                   *reinterpret_cast<const uint2 *>(pool + (at * PAGE + src % PAGE) * D + Page8<D>::col(lane)),
-                   layer.scales[2 * at + is_v]);
+            const int moved = root + node((t - root - 1) & 63);
+            const int src = t > root + k0 && t <= last ? moved : t;
+            // rows past the last one kept are not read: any place of the page will do
+            const int at = t <= last ? src : page * PAGE;
+            const int id = __shfl_sync(0xffffffffu, blk, at / PAGE - page0);
+            from[st] = id * PAGE + at % PAGE;  // below 2^31: num_blocks * 16 entries are within the pools
         }
-    }
-    __syncthreads();
-    if (mine) {
-        const size_t at = (size_t)tbl[page] * P.Hkv + h;
-        pg.store(pool + at * PAGE * D, layer.scales + 2 * at + is_v, min(PAGE, last + 1 - page * PAGE), lane);
+        const int dst = __shfl_sync(0xffffffffu, blk, page - page0);
+        const int kept = min(PAGE, last + 1 - page * PAGE);
+#pragma unroll 1
+        for (int j = first; j < jobs; j += stride) {
+            const int is_v = j & 1, h = (j >> 1) % P.Hkv;
+            const sv_kv_q8 &layer = P.layer[(j >> 1) / P.Hkv];
+            uint8_t *pool = static_cast<uint8_t *>(is_v ? layer.v_pool : layer.k_pool);
+            uint2 raw[Page8<D>::STEPS];
+            float scale[Page8<D>::STEPS];
+#pragma unroll
+            for (int st = 0; st < Page8<D>::STEPS; ++st) {
+                const size_t at = (size_t)(from[st] / PAGE) * P.Hkv + h;
+                raw[st] = *reinterpret_cast<const uint2 *>(pool + (at * PAGE + from[st] % PAGE) * D + Page8<D>::col(lane));
+                scale[st] = layer.scales[2 * at + is_v];
+            }
+            const size_t at = (size_t)dst * P.Hkv + h;
+            __syncwarp();  // every lane has read the page before one writes it
+            auto get = [&](int st, int i, float &x, float &y) { unpack_e4m3(raw[st], i, scale[st], x, y); };
+            const int e = page8_exponent(warp_max(Page8<D>::template top<Page8<D>::STEPS>(0, kept, lane, get)));
+            if (lane == 0) layer.scales[2 * at + is_v] = exp2_int(e);
+            Page8<D>::template write<Page8<D>::STEPS>(pool + at * PAGE * D, e, 0, kept, lane, get);
+        }
+        __syncwarp();
     }
 }
 
 }  // namespace
 
 cudaError_t launch_kv_commit_q8(const CommitQ8Launch &c, cudaStream_t stream) {
-    // pages that N - 1 consecutive positions can touch, two warps each (at most 10 for N = 64)
-    const unsigned pages = (unsigned)((c.N - 1 + PAGE - 2) / PAGE + 1);
-    const dim3 grid((unsigned)c.B, (unsigned)c.Hkv, (unsigned)c.L);
+    // A warp takes every stride-th job of its sequence: one each while the warps
+    // fit the SMs (about 24 a piece at this kernel's registers), more beyond.
+    const long long jobs = 2LL * c.Hkv * c.L, fit = 148LL * 24;
+    const long long per = (jobs * c.B + fit - 1) / fit;
+    const long long warps = (jobs + per - 1) / per;
+    const unsigned ctas = (unsigned)((warps + CQ_WARPS - 1) / CQ_WARPS);
+    const dim3 grid((unsigned)c.B, ctas);
+    const int stride = (int)ctas * CQ_WARPS;
     if (c.D == 128)
-        kv_commit_q8_kernel<128><<<grid, 64 * pages, 0, stream>>>(c);
+        kv_commit_q8_kernel<128><<<grid, 32 * CQ_WARPS, 0, stream>>>(c, stride);
     else
-        kv_commit_q8_kernel<64><<<grid, 64 * pages, 0, stream>>>(c);
+        kv_commit_q8_kernel<64><<<grid, 32 * CQ_WARPS, 0, stream>>>(c, stride);
     return cudaGetLastError();
 }
 

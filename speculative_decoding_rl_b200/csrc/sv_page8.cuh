@@ -37,6 +37,19 @@ SV_DEV uint32_t float2_to_e4m3x2(float a, float b) {
     return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
+// The e4m3 byte of x * inv, NaN for entries that are not finite.
+SV_DEV uint32_t page8_pair(float a, float b, float inv) {
+    a = fabsf(a) < INFINITY ? a * inv : NAN;
+    b = fabsf(b) < INFINITY ? b * inv : NAN;
+    return float2_to_e4m3x2(a, b);
+}
+
+// |x| where it is finite, else 0: NaN and infinities do not enter a scale.
+SV_DEV float page8_mag(float x) {
+    const float a = fabsf(x);
+    return a < INFINITY ? a : 0.f;
+}
+
 // A warp's view of a page: 8 consecutive entries of a row per lane and step,
 // D/8 lanes to a row, so a step covers 256 consecutive bytes of the page.
 template <int D>
@@ -44,53 +57,53 @@ struct Page8 {
     static constexpr int LANES_ROW = D / 8;
     static constexpr int ROWS_STEP = 32 / LANES_ROW;
     static constexpr int STEPS = PAGE / ROWS_STEP;
-    float val[STEPS][8];
 
     SV_DEV static int row(int step, int lane) { return step * ROWS_STEP + lane / LANES_ROW; }
     SV_DEV static int col(int lane) { return lane % LANES_ROW * 8; }
 
-    SV_DEV void set(int step, uint2 bytes, float scale) {
-        const uint32_t w[4] = {bytes.x, bytes.x >> 16, bytes.y, bytes.y >> 16};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 f = e4m3x2_to_float2(w[j]);
-            val[step][2 * j] = f.x * scale;
-            val[step][2 * j + 1] = f.y * scale;
-        }
-    }
-
-    // Scale of the rows [0, kept) and those rows written to `page` (16 x D bytes). Rows
-    // past `kept` are left as they were.
-    SV_DEV void store(uint8_t *page, float *scale, int kept, int lane) const {
+    // Steps [S0, S0 + NS) of a page's rows [0, kept). get(step, i, a, b) gives
+    // entries 2i and 2i + 1 of the lane's 8 of a step in fp32.
+    // Largest magnitude of the lane's entries:
+    template <int NS, typename Get>
+    SV_DEV static float top(int S0, int kept, int lane, Get get) {
         float amax = 0.f;
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s)
-            if (row(s, lane) < kept)
+        for (int s = 0; s < NS; ++s)
+            if (row(S0 + s, lane) < kept)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float a = fabsf(val[s][j]);
-                    amax = fmaxf(amax, a < INFINITY ? a : 0.f);  // NaN and infinities do not enter the scale
+                for (int i = 0; i < 4; ++i) {
+                    float a, b;
+                    get(s, i, a, b);
+                    amax = fmaxf(amax, fmaxf(page8_mag(a), page8_mag(b)));
                 }
-        amax = warp_max(amax);
-        const int e = page8_exponent(amax);
+        return amax;
+    }
+    // The rows under 2^e, to `page` (16 x D bytes); rows past `kept` stay as they were.
+    template <int NS, typename Get>
+    SV_DEV static void write(uint8_t *page, int e, int S0, int kept, int lane, Get get) {
         const float inv = exp2_int(-e);
-        if (lane == 0) *scale = exp2_int(e);
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-            const int r = row(s, lane);
+        for (int s = 0; s < NS; ++s) {
+            const int r = row(S0 + s, lane);
             if (r >= kept) continue;
             uint32_t w[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float a = val[s][2 * j], b = val[s][2 * j + 1];
-                a = fabsf(a) < INFINITY ? a * inv : NAN;
-                b = fabsf(b) < INFINITY ? b * inv : NAN;
-                w[j] = float2_to_e4m3x2(a, b);
+            for (int i = 0; i < 4; ++i) {
+                float a, b;
+                get(s, i, a, b);
+                w[i] = page8_pair(a, b, inv);
             }
-            *reinterpret_cast<uint2 *>(page + r * D + col(lane)) =
-                make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+            *reinterpret_cast<uint2 *>(page + r * D + col(lane)) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
         }
     }
 };
+
+// Entries 2i and 2i + 1 of 8 e4m3 bytes under a scale.
+SV_DEV void unpack_e4m3(uint2 bytes, int i, float scale, float &a, float &b) {
+    const uint32_t w = i < 2 ? bytes.x : bytes.y;
+    const float2 f = e4m3x2_to_float2(i & 1 ? w >> 16 : w);
+    a = f.x * scale;
+    b = f.y * scale;
+}
 
 }  // namespace sv

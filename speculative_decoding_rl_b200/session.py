@@ -11,10 +11,9 @@ from typing import Optional
 
 import torch
 
-from . import (SvAttnDesc, SvKVLayer, SvPagedKV, make_accept_desc, make_cascade_desc, make_kv_layers, make_kv_q8,
-               make_kv_q8_layers, make_new_rows, sv_accept, sv_accept_workspace_size,
-               sv_cascade_attention_workspace_size, sv_cascade_verify_attention, sv_kv_append, sv_kv_append_q8,
-               sv_kv_commit, sv_kv_commit_q8, sv_verify_attention, sv_verify_attention_q8,
+from . import (PreparedCall, SvAttnDesc, SvKVLayer, SvPagedKV, make_accept_desc, make_cascade_desc, make_kv_layers,
+               make_kv_q8, make_kv_q8_layers, make_new_rows, sv_accept, sv_accept_workspace_size,
+               sv_cascade_attention_workspace_size, sv_cascade_verify_attention, sv_kv_commit, sv_verify_attention,
                sv_verify_attention_q8_workspace_size, sv_verify_attention_workspace_size)
 
 
@@ -99,23 +98,20 @@ class AcceptCall:
 class CommitCall:
     """KV commit after accept over a fixed set of layers' pools (arguments prepared once)."""
 
-    _layers = staticmethod(make_kv_layers)
-    _call = staticmethod(sv_kv_commit)
-
     def __init__(self, desc, layers, block_table, ctx_lens, accept_len, accept_path, device: str = "cuda"):
         dev = torch.device(device)
         B = desc.num_seqs
         self.desc = desc
         self.layers = layers
-        self._arr = self._layers(layers)
+        self._arr = make_kv_layers(layers)
         self.block_table, self.ctx_lens = block_table, ctx_lens
         self.accept_len, self.accept_path = accept_len, accept_path
         self.new_ctx_lens = torch.empty(B, dtype=torch.int32, device=dev)
         self.status = torch.empty(B, dtype=torch.int32, device=dev)
 
     def run(self, stream=None):
-        self._call(self.desc, self._arr, self.block_table, self.ctx_lens, self.accept_len, self.accept_path,
-                   self.new_ctx_lens, self.status, stream)
+        sv_kv_commit(self.desc, self._arr, self.block_table, self.ctx_lens, self.accept_len, self.accept_path,
+                     self.new_ctx_lens, self.status, stream)
         return self.new_ctx_lens
 
 
@@ -124,7 +120,9 @@ class AppendCall:
 
     desc: SvAttnDesc with num_q_rows = N; rope: ``make_rope_desc``; kv: (k_pool, v_pool); q [B][N][Hq][D] or None,
     k and v [B][N][Hkv][D], possibly slices of a fused projection's output, read anew by every run(). q_out is
-    allocated unless given."""
+    allocated unless given. Every tensor is on one device, whose current stream run() uses unless given one."""
+
+    _entry = "sv_kv_append"
 
     def __init__(self, desc, rope, kv, block_table, ctx_lens, q, k, v, positions=None, new_lens=None,
                  q_out: Optional[torch.Tensor] = None):
@@ -133,31 +131,31 @@ class AppendCall:
             raise ValueError("the new rows' shapes do not match the descriptor")
         self.desc, self.rope = desc, rope
         self.rows = make_new_rows(q, k, v, positions, new_lens)
-        self.kv = self._cache(kv)
+        self.pools, self.kv = kv, self._cache(kv)
         self.block_table, self.ctx_lens = block_table, ctx_lens
         if q is not None and q_out is None:
             q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         self.q_out = q_out
         self.status = torch.empty(desc.num_seqs, dtype=torch.int32, device=k.device)
+        self._call = PreparedCall(self._entry, desc, rope, self.rows, self.kv, block_table, ctx_lens, q_out, self.status,
+                                  beside=(q, k, v, positions, new_lens, getattr(rope, "_keep", None), *kv))
 
-    _call = staticmethod(sv_kv_append)
-
-    def _cache(self, kv):
-        self.pools = kv
+    @staticmethod
+    def _cache(kv):
         return SvKVLayer(*(x.data_ptr() for x in kv))
 
     def run(self, stream=None) -> Optional[torch.Tensor]:
-        self._call(self.desc, self.rope, self.rows, self.kv, self.block_table, self.ctx_lens, self.q_out, self.status,
-                   stream)
+        self._call(stream)
         return self.q_out
 
 
 class AppendQ8Call(AppendCall):
     """AppendCall into a layer's 8-bit cache; kv: (k_pool, v_pool, scales)."""
 
-    _call = staticmethod(sv_kv_append_q8)
+    _entry = "sv_kv_append_q8"
 
-    def _cache(self, kv):
+    @staticmethod
+    def _cache(kv):
         return make_kv_q8(*kv)
 
 
@@ -166,21 +164,34 @@ class AttentionQ8Call:
 
     def __init__(self, desc, kv, block_table, ctx_lens, q, draft_mask=None, out: Optional[torch.Tensor] = None):
         self.desc = desc
-        self.kv = make_kv_q8(*kv)
+        self.pools, self.kv = kv, make_kv_q8(*kv)
         self.block_table, self.ctx_lens, self.q, self.mask = block_table, ctx_lens, q, draft_mask
         self.out = out if out is not None else torch.empty_like(q)
         self.status = torch.empty(desc.num_seqs, dtype=torch.int32, device=q.device)
-        self.ws_bytes = sv_verify_attention_q8_workspace_size(desc)
+        with torch.cuda.device(q.device):
+            self.ws_bytes = sv_verify_attention_q8_workspace_size(desc)
         self.workspace = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=q.device)
+        self._call = PreparedCall("sv_verify_attention_q8", desc, q, self.kv, block_table, ctx_lens, draft_mask,
+                                  self.out, self.workspace, self.ws_bytes, self.status, beside=kv)
 
     def run(self, stream=None) -> torch.Tensor:
-        sv_verify_attention_q8(self.desc, self.q, self.kv, self.block_table, self.ctx_lens, self.mask, self.out,
-                               self.workspace, self.ws_bytes, self.status, stream)
+        self._call(stream)
         return self.out
 
 
-class CommitQ8Call(CommitCall):
+class CommitQ8Call:
     """KV commit after accept over the 8-bit caches of all layers; layers: (k_pool, v_pool, scales) each."""
 
-    _layers = staticmethod(make_kv_q8_layers)
-    _call = staticmethod(sv_kv_commit_q8)
+    def __init__(self, desc, layers, block_table, ctx_lens, accept_len, accept_path):
+        self.desc, self.layers = desc, layers
+        self.block_table, self.ctx_lens = block_table, ctx_lens
+        self.accept_len, self.accept_path = accept_len, accept_path
+        self.new_ctx_lens = torch.empty(desc.num_seqs, dtype=torch.int32, device=ctx_lens.device)
+        self.status = torch.empty(desc.num_seqs, dtype=torch.int32, device=ctx_lens.device)
+        self._call = PreparedCall("sv_kv_commit_q8", desc, len(layers), make_kv_q8_layers(layers), block_table,
+                                  ctx_lens, accept_len, accept_path, self.new_ctx_lens, self.status,
+                                  beside=[x for layer in layers for x in layer])
+
+    def run(self, stream=None) -> torch.Tensor:
+        self._call(stream)
+        return self.new_ctx_lens
