@@ -176,10 +176,10 @@ SV_DEV void rotate_row(const AppendParams &p, int b, int i, int tid, int group) 
     if (!s.ok || i >= s.n) return;
     const PageRows pr(p, s, b, (s.start + i) / PAGE);
     const int t = __shfl_sync(0xffffffffu, pr.pos, i - pr.i0);
-    if (!pr.ok(p)) return;
     Turn turn;
     turn.on = false;
-    if (p.R > 0) turn.load(p, t, c);
+    if (p.R > 0) turn.load(p, max(0, min(t, p.max_position - 1)), c);  // a position outside skips the page below
+    if (!pr.ok(p)) return;
     const bool pairs = !p.interleaved && p.R > 0;  // with the chunk pair_chunk, for the chunks that turn
     const bool near = 32 % chunks == 0;            // which a lane of the warp holds
     const int pc = turn.on ? pair_chunk(p, c) : c, mate = (int)(threadIdx.x & 31) - c + pc;
@@ -314,7 +314,7 @@ SV_DEV void append_page(const AppendParams &p, int b, int index, int job, bool h
     if (!has_job) return;
     const int e = page8_exponent(fmaxf(tops[warp], tops[warp ^ 1]));
     if (lane == 0 && !(warp & 1)) *scale = exp2_int(e);
-    Pg::template write<NS>(dst, e, S0, kept, lane, get);
+    Pg::template write<NS>(dst, e, S0, kept, lane, get, [](int) { return false; });
 }
 
 // Grid: (pages a sequence's rows can touch x kv_parts, then its rows; sequences).
@@ -346,6 +346,7 @@ cudaError_t launch_append(const AppendParams &p, bool q8, cudaStream_t stream) {
     }
     const int pages = (p.N + PAGE - 2) / PAGE + 1;  // that N consecutive positions can touch
     const int kv_parts = (2 * p.Hkv + AP_WARPS / 2 - 1) / (AP_WARPS / 2);
+    if ((long long)pages * kv_parts + row_ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     const dim3 grid((unsigned)pages * kv_parts + (p.q ? row_ctas : 0u), (unsigned)p.B);
     if (p.D == 128)
         append_q8_kernel<128><<<grid, AP_THREADS, 0, stream>>>(p, pages, kv_parts, rows);

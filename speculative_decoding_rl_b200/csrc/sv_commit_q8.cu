@@ -13,7 +13,8 @@
 // The call moves little; what bounds it is the chain of loads (lengths and
 // path, then block ids, then rows and scales) and the number of warps that run
 // through it. A warp therefore does all jobs it is given after one walk of the
-// first two steps, as many as make the grid fill the SMs about once.
+// first two steps, as many as make the grid fill the SMs about once. Rows that
+// stay under a scale that stays are read for the scale, but not written.
 #include "sv_page8.cuh"
 #include "sv_q8.h"
 
@@ -67,6 +68,7 @@ __global__ void __launch_bounds__(32 * CQ_WARPS, 3) kv_commit_q8_kernel(const __
     for (int page = (root + 1 + k0) / PAGE; page <= last / PAGE; ++page) {
         // where the rows of this lane come from: page's index among the loaded ids and row
         int from[Page8<D>::STEPS];
+        uint32_t stays = 0;  // steps whose row does not move
 #pragma unroll
         for (int st = 0; st < Page8<D>::STEPS; ++st) {
             const int t = page * PAGE + Page8<D>::row(st, lane);
@@ -75,6 +77,7 @@ __global__ void __launch_bounds__(32 * CQ_WARPS, 3) kv_commit_q8_kernel(const __
             // rows past the last one kept are not read: any place of the page will do
             const int at = t <= last ? src : page * PAGE;
             const int id = __shfl_sync(0xffffffffu, blk, at / PAGE - page0);
+            stays |= (uint32_t)(at == t) << st;
             from[st] = id * PAGE + at % PAGE;  // below 2^31: num_blocks * 16 entries are within the pools
         }
         const int dst = __shfl_sync(0xffffffffu, blk, page - page0);
@@ -97,7 +100,8 @@ __global__ void __launch_bounds__(32 * CQ_WARPS, 3) kv_commit_q8_kernel(const __
             auto get = [&](int st, int i, float &x, float &y) { unpack_e4m3(raw[st], i, scale[st], x, y); };
             const int e = page8_exponent(warp_max(Page8<D>::template top<Page8<D>::STEPS>(0, kept, lane, get)));
             if (lane == 0) layer.scales[2 * at + is_v] = exp2_int(e);
-            Page8<D>::template write<Page8<D>::STEPS>(pool + at * PAGE * D, e, 0, kept, lane, get);
+            Page8<D>::template write<Page8<D>::STEPS>(pool + at * PAGE * D, e, 0, kept, lane, get,
+                                                            [&](int st) { return stays >> st & 1 && scale[st] == exp2_int(e); });
         }
         __syncwarp();
     }

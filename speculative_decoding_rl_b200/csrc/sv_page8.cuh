@@ -78,14 +78,15 @@ struct Page8 {
                 }
         return amax;
     }
-    // The rows under 2^e, to `page` (16 x D bytes); rows past `kept` stay as they were.
-    template <int NS, typename Get>
-    SV_DEV static void write(uint8_t *page, int e, int S0, int kept, int lane, Get get) {
+    // The rows under 2^e, to `page` (16 x D bytes), but for those that are(step)
+    // says are there already; rows past `kept` stay as they were.
+    template <int NS, typename Get, typename Are>
+    SV_DEV static void write(uint8_t *page, int e, int S0, int kept, int lane, Get get, Are are) {
         const float inv = exp2_int(-e);
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
             const int r = row(S0 + s, lane);
-            if (r >= kept) continue;
+            if (r >= kept || are(s)) continue;
             uint32_t w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
