@@ -8,7 +8,7 @@
 // fp32, bit for bit, whatever the compiler does.
 //
 // q, and K and V of the bf16 call: a CTA takes one row (or a few, where a row has
-// few heads), a thread 8 entries (16 bytes) of up to AP_BATCH heads at a time and
+// few heads), a thread the same 16 entries of up to AP_BATCH heads at a time and
 // their cosines and sines once. K and V of the 8-bit call: a page's scale is the
 // maximum over its rows, so two warps take the page of one KV head, K or V.
 // Little is computed; what bounds a call is memory when there are many rows, and
@@ -81,95 +81,118 @@ struct PageRows {
     }
 };
 
-// The cosines and sines that 8 entries [8c, 8c + 8) of a head turn by.
+// A head is taken in slots of two chunks of 8 entries (16 bytes). Slot s < R/16
+// holds entries that turn by the angles [8s, 8s + 8): chunks s and s + R/16 in
+// the half layout, 2s and 2s + 1 in the interleaved one. The slots behind hold
+// the entries that do not turn, two chunks each (the last one may have one).
+struct Slot {
+    int c1, c2;
+    bool turns, two;
+    SV_DEV Slot(const AppendParams &p, int s) {
+        const int n = p.R / 16;
+        turns = s < n;
+        c1 = turns ? (p.interleaved ? 2 * s : s) : p.R / 8 + 2 * (s - n);
+        c2 = turns && !p.interleaved ? s + n : c1 + 1;
+        two = 8 * c2 < p.D;
+    }
+};
+
+// Two fp32 products per instruction, each rounded by itself.
+SV_DEV float2 mul2(float a0, float a1, uint64_t b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, d;\n\tmov.b64 a, {%2, %3};\n\tmul.rn.f32x2 d, a, %4;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a0), "f"(a1), "l"(b));
+    return d;
+}
+
+// The cosines and sines of a slot at position t.
 struct Turn {
-    float cs[8], sn[8];  // interleaved: the first four of each
-    bool on;
-    SV_DEV void load(const AppendParams &p, int t, int c) {
-        on = 8 * c < p.R;
-        if (!on) return;
-        const float *row = p.cos_sin + (size_t)t * p.R;
-        const int half = p.R / 2;
-        if (p.interleaved) {
-            *reinterpret_cast<float4 *>(cs) = __ldg(reinterpret_cast<const float4 *>(row + 4 * c));
-            *reinterpret_cast<float4 *>(sn) = __ldg(reinterpret_cast<const float4 *>(row + half + 4 * c));
-        } else {
-            const int j = 8 * c < half ? 8 * c : 8 * c - half;
+    ulonglong2 cs[2], sn[2];
+    SV_DEV void load(const AppendParams &p, int t, int s) {
+        const float *row = p.cos_sin + (size_t)t * p.R + 8 * s;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                reinterpret_cast<float4 *>(cs)[k] = __ldg(reinterpret_cast<const float4 *>(row + j) + k);
-                reinterpret_cast<float4 *>(sn)[k] = __ldg(reinterpret_cast<const float4 *>(row + half + j) + k);
-            }
+        for (int k = 0; k < 2; ++k) {
+            cs[k] = __ldg(reinterpret_cast<const ulonglong2 *>(row) + k);
+            sn[k] = __ldg(reinterpret_cast<const ulonglong2 *>(row + p.R / 2) + k);
         }
     }
 };
 
-SV_DEV void unpack8(uint4 u, float *x) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+SV_DEV float low_bf16(uint32_t w) { return __uint_as_float(w << 16); }
+SV_DEV float high_bf16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// A slot's 16 entries in memory order, in fp32.
+SV_DEV void unpack_slot(const uint4 &u1, const uint4 &u2, float *y) {
+    const uint32_t w[8] = {u1.x, u1.y, u1.z, u1.w, u2.x, u2.y, u2.z, u2.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        x[2 * j] = __uint_as_float(w[j] << 16);
-        x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    for (int j = 0; j < 8; ++j) {
+        y[2 * j] = __uint_as_float(w[j] << 16);
+        y[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
     }
 }
 
-SV_DEV uint4 pack8(const float *x) {
-    uint32_t w[4];
+// (x1 c - x2 s, x2 c + x1 s) for the slot's 8 pairs: entries j and 8 + j in the
+// half layout, 2j and 2j + 1 in the interleaved one. The sums are scalar, so that
+// no compiler contracts them with the products.
+template <bool INTERLEAVED>
+SV_DEV void turn_slot(const Turn &t, float *y) {
+    const uint64_t cs[4] = {t.cs[0].x, t.cs[0].y, t.cs[1].x, t.cs[1].y};
+    const uint64_t sn[4] = {t.sn[0].x, t.sn[0].y, t.sn[1].x, t.sn[1].y};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+    for (int j = 0; j < 8; j += 2) {
+        float &a0 = y[INTERLEAVED ? 2 * j : j], &a1 = y[INTERLEAVED ? 2 * j + 2 : j + 1];
+        float &b0 = y[INTERLEAVED ? 2 * j + 1 : 8 + j], &b1 = y[INTERLEAVED ? 2 * j + 3 : 9 + j];
+        const float2 ac = mul2(a0, a1, cs[j / 2]), bs = mul2(b0, b1, sn[j / 2]);
+        const float2 bc = mul2(b0, b1, cs[j / 2]), as = mul2(a0, a1, sn[j / 2]);
+        a0 = __fsub_rn(ac.x, bs.x);
+        a1 = __fsub_rn(ac.y, bs.y);
+        b0 = __fadd_rn(bc.x, as.x);
+        b1 = __fadd_rn(bc.y, as.y);
+    }
+}
+
+// Turns a slot in bf16, rounding once.
+template <bool INTERLEAVED>
+SV_DEV void turn_bf16(const Turn &t, uint4 &u1, uint4 &u2) {
+    float y[16];
+    unpack_slot(u1, u2, y);
+    turn_slot<INTERLEAVED>(t, y);
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
         w[j] = *reinterpret_cast<const uint32_t *>(&h);
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    u1 = make_uint4(w[0], w[1], w[2], w[3]);
+    u2 = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
-// x: entries [8c, 8c+8) of a head; other: in the half layout the entries they pair with.
-SV_DEV void turn8(const AppendParams &p, const Turn &t, int c, float *x, const float *other) {
-    if (!t.on) return;
-    if (p.interleaved) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float a = x[2 * j], b = x[2 * j + 1];
-            x[2 * j] = __fsub_rn(__fmul_rn(a, t.cs[j]), __fmul_rn(b, t.sn[j]));
-            x[2 * j + 1] = __fadd_rn(__fmul_rn(b, t.cs[j]), __fmul_rn(a, t.sn[j]));
-        }
-    } else if (16 * c < p.R) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = __fsub_rn(__fmul_rn(x[j], t.cs[j]), __fmul_rn(other[j], t.sn[j]));
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = __fadd_rn(__fmul_rn(x[j], t.cs[j]), __fmul_rn(other[j], t.sn[j]));
-    }
-}
-
-// Chunk that chunk c pairs with in the half layout.
-SV_DEV int pair_chunk(const AppendParams &p, int c) { return 16 * c < p.R ? c + p.R / 16 : c - p.R / 16; }
-
-constexpr int AP_BATCH = 4;
+constexpr int AP_BATCH = 2;  // heads of a thread in flight
 
 // Heads of row i of sequence b by `group` threads (whole warps): q to q_out, and
 // (KV) k and v to their page of the bf16 cache.
 template <bool KV>
 SV_DEV void rotate_row(const AppendParams &p, int b, int i, int tid, int group) {
-    const int chunks = p.D / 8;
-    const int lanes = group / chunks;  // heads in flight
-    const int c = tid % chunks, h0 = tid / chunks;
+    const int lanes = group / p.slots;  // heads in flight
+    const int h0 = tid / p.slots, sl = tid - h0 * p.slots;
+    const Slot slot(p, sl);
     const size_t row = (size_t)b * p.N + i;
     const int hq = p.q ? p.Hq : 0;
-    // D / 8 need not divide the group; rows past new_lens are not read
+    // the slots need not divide the group; rows past new_lens are not read
     const int n = p.new_lens ? p.new_lens[b] : p.N;
     const int heads = h0 < lanes && i < n && i < p.N ? hq + (KV ? 2 * p.Hkv : 0) : 0;
-    auto source = [&](int h) {
-        const int hk = h >= hq + p.Hkv ? h - hq - p.Hkv : h - hq;
-        const uint16_t *src = h < hq ? p.q + row * p.q_stride + (size_t)h * p.D
-                                     : (h >= hq + p.Hkv ? p.v : p.k) + row * p.kv_stride + (size_t)hk * p.D;
-        return reinterpret_cast<const uint4 *>(src);
-    };
-    uint4 own[AP_BATCH];
+    uint4 u1[AP_BATCH], u2[AP_BATCH];
     auto fetch = [&](int h) {
 #pragma unroll
-        for (int k = 0; k < AP_BATCH; ++k)
-            if (h + k * lanes < heads) own[k] = __ldg(source(h + k * lanes) + c);
+        for (int k = 0; k < AP_BATCH; ++k, h += lanes)
+            if (h < heads) {
+                const uint16_t *src = h < hq ? p.q + row * p.q_stride + h * p.D
+                                             : (h >= hq + p.Hkv ? p.v + row * p.kv_stride + (h - hq - p.Hkv) * p.D
+                                                                : p.k + row * p.kv_stride + (h - hq) * p.D);
+                u1[k] = __ldg(reinterpret_cast<const uint4 *>(src) + slot.c1);
+                if (slot.two) u2[k] = __ldg(reinterpret_cast<const uint4 *>(src) + slot.c2);
+            }
     };
     fetch(h0);
     const Seq s = read_seq(p, b);
@@ -177,50 +200,26 @@ SV_DEV void rotate_row(const AppendParams &p, int b, int i, int tid, int group) 
     const PageRows pr(p, s, b, (s.start + i) / PAGE);
     const int t = __shfl_sync(0xffffffffu, pr.pos, i - pr.i0);
     Turn turn;
-    turn.on = false;
-    if (p.R > 0) turn.load(p, max(0, min(t, p.max_position - 1)), c);  // a position outside skips the page below
+    if (slot.turns) turn.load(p, max(0, min(t, p.max_position - 1)), sl);  // a position outside skips the page below
     if (!pr.ok(p)) return;
-    const bool pairs = !p.interleaved && p.R > 0;  // with the chunk pair_chunk, for the chunks that turn
-    const bool near = 32 % chunks == 0;            // which a lane of the warp holds
-    const int pc = turn.on ? pair_chunk(p, c) : c, mate = (int)(threadIdx.x & 31) - c + pc;
-    const int at = (s.start + i) % PAGE;
-    const int rounds = (hq + (KV ? 2 * p.Hkv : 0) + AP_BATCH * lanes - 1) / (AP_BATCH * lanes);
+    const size_t page = (size_t)pr.blk * p.Hkv * PAGE + (s.start + i) % PAGE;  // row of the cache, of KV head 0
 #pragma unroll 1
-    for (int r = 0; r < rounds; ++r) {
-        const int h = h0 + r * AP_BATCH * lanes;
-        if (r) fetch(h);
+    for (int h = h0; h < heads; h += AP_BATCH * lanes) {
+        if (h != h0) fetch(h);
 #pragma unroll
         for (int k = 0; k < AP_BATCH; ++k) {
             const int hh = h + k * lanes;
-            const bool is_q = hh < hq, is_v = hh >= hq + p.Hkv;
-            uint4 m = own[k];
-            if (pairs) {
-                if (near) {
-                    m.x = __shfl_sync(0xffffffffu, own[k].x, mate);
-                    m.y = __shfl_sync(0xffffffffu, own[k].y, mate);
-                    m.z = __shfl_sync(0xffffffffu, own[k].z, mate);
-                    m.w = __shfl_sync(0xffffffffu, own[k].w, mate);
-                } else if (hh < heads) {
-                    m = __ldg(source(hh) + pc);
-                }
+            if (hh >= heads) break;
+            const bool is_v = hh >= hq + p.Hkv;
+            if (slot.turns && !is_v) {
+                if (p.interleaved) turn_bf16<true>(turn, u1[k], u2[k]);
+                else turn_bf16<false>(turn, u1[k], u2[k]);
             }
-            if (hh >= heads) continue;
-            const int hk = is_v ? hh - hq - p.Hkv : hh - hq;
-            if (turn.on && !is_v) {
-                float x[8], o[8];
-                unpack8(own[k], x);
-                unpack8(m, o);
-                turn8(p, turn, c, x, o);
-                own[k] = pack8(x);
-            }
-            uint16_t *dst;
-            if (is_q) {
-                dst = p.q_out + (row * p.Hq + hh) * p.D;
-            } else {
-                uint16_t *pool = static_cast<uint16_t *>(is_v ? p.v_pool : p.k_pool);
-                dst = pool + (((size_t)pr.blk * p.Hkv + hk) * PAGE + at) * p.D;
-            }
-            reinterpret_cast<uint4 *>(dst)[c] = own[k];
+            uint16_t *dst = hh < hq ? p.q_out + (row * p.Hq + hh) * p.D
+                                    : is_v ? static_cast<uint16_t *>(p.v_pool) + (page + (hh - hq - p.Hkv) * PAGE) * p.D
+                                           : static_cast<uint16_t *>(p.k_pool) + (page + (hh - hq) * PAGE) * p.D;
+            reinterpret_cast<uint4 *>(dst)[slot.c1] = u1[k];
+            if (slot.two) reinterpret_cast<uint4 *>(dst)[slot.c2] = u2[k];
         }
     }
 }
@@ -228,9 +227,9 @@ SV_DEV void rotate_row(const AppendParams &p, int b, int i, int tid, int group) 
 // Rows a CTA takes: as many as leave a thread no more than one batch of a row's
 // heads, in whole warps.
 int rows_per_cta(const AppendParams &p, bool kv) {
-    const int items = ((p.q ? p.Hq : 0) + (kv ? 2 * p.Hkv : 0)) * (p.D / 8);
+    const int items = ((p.q ? p.Hq : 0) + (kv ? 2 * p.Hkv : 0)) * p.slots;
     int rows = 1;
-    while (rows < AP_WARPS && AP_THREADS / (2 * rows) * AP_BATCH >= items && AP_THREADS / (2 * rows) >= p.D / 8) rows *= 2;
+    while (rows < AP_WARPS && AP_THREADS / (2 * rows) * AP_BATCH >= items && AP_THREADS / (2 * rows) >= p.slots) rows *= 2;
     return rows;
 }
 
@@ -244,77 +243,78 @@ __global__ void __launch_bounds__(AP_THREADS, 4) append_kernel(const __grid_cons
 // whole CTA comes here for one page. tops: a float per warp.
 template <int D>
 SV_DEV void append_page(const AppendParams &p, int b, int index, int job, bool has_job, int warp, int lane, float *tops) {
-    using Pg = Page8<D>;
-    constexpr int NS = Pg::STEPS / 2;
+    // a lane holds one slot (two chunks) of NS of the page's rows
+    constexpr int SLOTS = D / 16, ROWS = 32 / SLOTS, NS = PAGE / 2 / ROWS;
     const Seq s = read_seq(p, b);
     const int page = s.start / PAGE + index;
     if (!s.ok || s.n == 0 || page * PAGE >= s.C) return;
-    const int hk = job >> 1, S0 = (warp & 1) * NS;
+    const int hk = job >> 1;
     const bool is_v = job & 1;
     const uint16_t *src = (is_v ? p.v : p.k) + (size_t)b * p.N * p.kv_stride + (size_t)hk * D;
-    const int c = Pg::col(lane) / 8;
-    const bool turns = !is_v && 8 * c < p.R, pairs = turns && !p.interleaved;
-    // the lane of this lane's row that holds the paired chunk
-    const int mate = lane - c + (pairs ? pair_chunk(p, c) : c);
+    const int sl = lane % SLOTS, r0 = (warp & 1) * (PAGE / 2) + lane / SLOTS;  // rows r0, r0 + ROWS, ..
+    const Slot slot(p, sl);
+    const bool turns = slot.turns && !is_v;
     const int first = page * PAGE - s.start;  // the new row on the page's row 0, if there is one
-    uint4 own[NS];
+    uint4 u1[NS], u2[NS];
 #pragma unroll
     for (int st = 0; st < NS; ++st) {
-        const int i = first + Pg::row(S0 + st, lane);
-        own[st] = make_uint4(0, 0, 0, 0);
-        if (has_job && i >= 0 && i < s.n) own[st] = __ldg(reinterpret_cast<const uint4 *>(src + i * p.kv_stride) + c);
+        const int i = first + r0 + st * ROWS;
+        u1[st] = u2[st] = make_uint4(0, 0, 0, 0);
+        if (has_job && i >= 0 && i < s.n) {
+            const uint4 *row = reinterpret_cast<const uint4 *>(src + i * p.kv_stride);
+            u1[st] = __ldg(row + slot.c1);
+            u2[st] = __ldg(row + slot.c2);
+        }
     }
     const PageRows pr(p, s, b, page);
     if (!pr.ok(p)) return;  // the same for every warp of the CTA
     uint8_t *dst = static_cast<uint8_t *>(is_v ? p.v_pool : p.k_pool) + ((size_t)pr.blk * p.Hkv + hk) * PAGE * D;
     float *scale = p.scales + ((size_t)pr.blk * p.Hkv + hk) * 2 + (is_v ? 1 : 0);
-    float val[NS][8];
-    if (has_job && first < 0) {  // rows that are there already
-        const float old_scale = *scale;
-#pragma unroll
-        for (int st = 0; st < NS; ++st) {
-            const int r = Pg::row(S0 + st, lane);
-            if (first + r < 0) {
-                const uint2 bytes = *reinterpret_cast<const uint2 *>(dst + r * D + 8 * c);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) unpack_e4m3(bytes, j, old_scale, val[st][2 * j], val[st][2 * j + 1]);
-            }
-        }
-    }
+    const int kept = min(PAGE, s.C - page * PAGE);
+    const float old_scale = has_job && first < 0 ? *scale : 0.f;  // of rows that are there already
+    float y[NS][16], top = 0.f;
 #pragma unroll
     for (int st = 0; st < NS; ++st) {
-        const int i = first + Pg::row(S0 + st, lane);
-        float o[8];
-        if (!is_v && !p.interleaved) {
-            uint4 m;
-            m.x = __shfl_sync(0xffffffffu, own[st].x, mate);
-            m.y = __shfl_sync(0xffffffffu, own[st].y, mate);
-            m.z = __shfl_sync(0xffffffffu, own[st].z, mate);
-            m.w = __shfl_sync(0xffffffffu, own[st].w, mate);
-            unpack8(m, o);
-        }
+        const int r = r0 + st * ROWS, i = first + r;
         const int t = __shfl_sync(0xffffffffu, pr.pos, (i - pr.i0) & 31);
-        if (i >= 0) {
-            unpack8(own[st], val[st]);
+        if (i < 0 && has_job) {
+            const uint2 b1 = reinterpret_cast<const uint2 *>(dst + r * D)[slot.c1];
+            const uint2 b2 = reinterpret_cast<const uint2 *>(dst + r * D)[slot.c2];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                unpack_e4m3(b1, j, old_scale, y[st][2 * j], y[st][2 * j + 1]);
+                unpack_e4m3(b2, j, old_scale, y[st][8 + 2 * j], y[st][9 + 2 * j]);
+            }
+        } else {
+            unpack_slot(u1[st], u2[st], y[st]);
             if (turns && i < s.n) {
                 Turn tn;
-                tn.load(p, t, c);
-                turn8(p, tn, c, val[st], o);
+                tn.load(p, t, sl);
+                if (p.interleaved) turn_slot<true>(tn, y[st]);
+                else turn_slot<false>(tn, y[st]);
             }
         }
+        if (r < kept)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) top = fmaxf(top, page8_mag(y[st][j]));
     }
-    const int kept = min(PAGE, s.C - page * PAGE);
-    auto get = [&](int st, int j, float &x, float &y) {
-        x = val[st][2 * j];
-        y = val[st][2 * j + 1];
-    };
-    const float top = warp_max(has_job ? Pg::template top<NS>(S0, kept, lane, get) : 0.f);
+    top = warp_max(has_job ? top : 0.f);
     if (lane == 0) tops[warp] = top;
     __syncthreads();  // both halves have read the page and its scale before one writes
     if (!has_job) return;
     const int e = page8_exponent(fmaxf(tops[warp], tops[warp ^ 1]));
+    const float inv = exp2_int(-e);
     if (lane == 0 && !(warp & 1)) *scale = exp2_int(e);
-    Pg::template write<NS>(dst, e, S0, kept, lane, get, [](int) { return false; });
+#pragma unroll
+    for (int st = 0; st < NS; ++st) {
+        const int r = r0 + st * ROWS;
+        if (r >= kept) continue;
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = page8_pair(y[st][2 * j], y[st][2 * j + 1], inv);
+        reinterpret_cast<uint2 *>(dst + r * D)[slot.c1] = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+        reinterpret_cast<uint2 *>(dst + r * D)[slot.c2] = make_uint2(w[4] | w[5] << 16, w[6] | w[7] << 16);
+    }
 }
 
 // Grid: (pages a sequence's rows can touch x kv_parts, then its rows; sequences).
@@ -337,7 +337,9 @@ __global__ void __launch_bounds__(AP_THREADS, 3) append_q8_kernel(const __grid_c
 
 }  // namespace
 
-cudaError_t launch_append(const AppendParams &p, bool q8, cudaStream_t stream) {
+cudaError_t launch_append(const AppendParams &params, bool q8, cudaStream_t stream) {
+    AppendParams p = params;
+    p.slots = p.R / 16 + ((p.D - p.R) / 8 + 1) / 2;
     const int rows = rows_per_cta(p, !q8);
     const unsigned row_ctas = (unsigned)((p.N + rows - 1) / rows);
     if (!q8) {

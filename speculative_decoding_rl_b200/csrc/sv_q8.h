@@ -18,6 +18,7 @@ struct AppendParams {
     float *scales;                 // [num_blocks][Hkv][2] (8-bit cache)
     int32_t *status;
     int B, N, Hq, Hkv, D, R, interleaved, max_position, max_blocks, num_blocks;
+    int slots;                     // of a head (set by launch_append)
 };
 cudaError_t launch_append(const AppendParams &p, bool q8, cudaStream_t stream);
 
