@@ -776,7 +776,7 @@ SV_DEV int block_sum_i(int v, int *red) {
 // ways or more, and the extra registers keep more of its partials' loads in
 // flight); three otherwise (a unit has a few partials, and most of the
 // combine's CTAs return after the schedule test, so CTA turnover counts).
-template <int MIN_CTAS>
+template <int MIN_CTAS, int UC>
 __global__ void __launch_bounds__(32 * COMBINE_ROWS, MIN_CTAS) attn_combine_kernel(const AttnParams p) {
     griddep_launch_dependents();  // the next call's attention kernel may run its prologue
     const int u = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -791,10 +791,10 @@ __global__ void __launch_bounds__(32 * COMBINE_ROWS, MIN_CTAS) attn_combine_kern
     // b's own tiles
     int tot = 0, before = 0, own = 0;
     for (int s = threadIdx.x; s < p.B; s += blockDim.x) {
-        const int t = seq_slots(p, s);
+        const int t = seq_slots<UC>(p, s);
         tot += t;
         before += s < b ? t : 0;
-        own += s == b ? real_tiles(t) : 0;
+        own += s == b ? real_tiles<UC>(t) : 0;
     }
     tot = block_sum_i(tot, red_i);
     before = block_sum_i(before, red_i);
@@ -806,7 +806,7 @@ __global__ void __launch_bounds__(32 * COMBINE_ROWS, MIN_CTAS) attn_combine_kern
     if (Tb == 0 || r >= rows) return;
     const int total = ups * tot;
     const int W = schedule_width(p, total);
-    const int tpre = ups * before + hr * (Tb + UNIT_COST);
+    const int tpre = ups * before + hr * (Tb + UC);
     const int first = tpre / W, n = (tpre + Tb - 1) / W - first + 1;
     if (n == 1) return;  // written by the attention kernel
     const int ridx = rc * RU + r;
@@ -1002,13 +1002,16 @@ cudaError_t launch_attention(const AttnParams &p, cudaStream_t stream) {
     const int RP = RU > 64 ? 96 : (RU + 15) / 16 * 16;
     cudaError_t e = p.D == 128 ? launch_tc_rp<128>(P, RP, stream) : launch_tc_rp<64>(P, RP, stream);
     if (e != cudaSuccess || p.all_slots) return e;  // a cascade call merges in the shared-prefix kernel
-    return launch_combine(p, stream);
+    return launch_combine<>(p, stream);
 }
 
+template <int UC>
 cudaError_t launch_combine(const AttnParams &p, cudaStream_t stream) {
-    return launch_programmatic(4 * p.units <= p.num_ctas ? attn_combine_kernel<2> : attn_combine_kernel<3>,
+    return launch_programmatic(4 * p.units <= p.num_ctas ? attn_combine_kernel<2, UC> : attn_combine_kernel<3, UC>,
                                dim3((p.rows_unit + COMBINE_ROWS - 1) / COMBINE_ROWS, p.units),
                                dim3(32 * COMBINE_ROWS), 0, stream, p);
 }
+template cudaError_t launch_combine<UNIT_COST>(const AttnParams &p, cudaStream_t stream);
+template cudaError_t launch_combine<UNIT_COST_Q8>(const AttnParams &p, cudaStream_t stream);
 
 }  // namespace sv

@@ -74,6 +74,7 @@ struct Q8Shape {
     static constexpr int THREADS = 32 * (MATH_WARPS + 3 * NT);
 };
 
+constexpr int UC = UNIT_COST_Q8;
 constexpr int SC_BATCH = 4;    // tiles whose page scales are fetched together
 constexpr int SC_RING = 4;     // batches of a range in shared memory
 constexpr int PAGES_TILE = TILE_KEYS / PAGE;
@@ -252,8 +253,9 @@ SV_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 }
 
 // Bounded wait on a phase, in few instructions (there are two dozen of them in
-// the kernel): gives up after WAIT_TRIES tries, each of which the hardware
-// suspends for a while, or once another thread has raised *abort; raises it then.
+// the kernel): gives up after WAIT_TRIES tries, which take a second or a few, or
+// once another thread has raised *abort; raises it then. (A suspend-time hint and
+// sleeps between the tries of the warps that feed the softmax measured the same.)
 constexpr uint32_t WAIT_TRIES = 1u << 23;
 SV_DEV bool wait_phase(uint64_t *b, uint32_t parity, volatile int *abort) {
     bool done = mbar_try_wait(b, parity);
@@ -348,7 +350,7 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
     }
     griddep_wait();  // no input is read, and nothing written, before this wait
     griddep_launch_dependents();
-    tile_prefix(p, TP, scratch, CL);  // contains __syncthreads
+    tile_prefix<UC>(p, TP, scratch, CL);  // contains __syncthreads
     const int ups = p.Hkv * p.RC;
     const int total = ups * TP[p.B];
     const int W = schedule_width(p, total);
@@ -357,7 +359,7 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
         const int v0 = (int)min((long long)(blockIdx.x + tid * gridDim.x) * W, (long long)total);
         const int v1 = min(v0 + W, total);
         int n;
-        const TileInfo t0 = cta_tiles(TP, p.B, ups, v0, v1, &n);
+        const TileInfo t0 = cta_tiles<UC>(TP, p.B, ups, v0, v1, &n);
         int *o = scratch + 8 * tid;
         o[0] = t0.b; o[1] = t0.hr; o[2] = t0.j; o[3] = t0.Tb; o[4] = n;
     }
@@ -404,7 +406,7 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
             TileInfo mine = ta;
 #pragma unroll 1
             for (int j = 1; j <= SC_BATCH; ++j) {
-                next_tile(ta, TP, p.B, ups);
+                next_tile<UC>(ta, TP, p.B, ups);
                 if (lane / PAGES_TILE >= j) mine = ta;
             }
             const int page = mine.j * PAGES_TILE + lane % PAGES_TILE;
@@ -454,7 +456,7 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
             // (pages wholly past ctx_len were loaded as zeros by the TMA unit)
             const int kn = max(0, C - p.N - ti.j * TILE_KEYS), k0 = max(0, C - ti.j * TILE_KEYS);
             const int k1 = min(TILE_KEYS, (k0 + PAGE - 1) / PAGE * PAGE);
-            next_tile(ti, TP, p.B, ups);
+            next_tile<UC>(ti, TP, p.B, ups);
             if (!(ok = wait_w(&v_full[vs], vph))) break;
             if (kn < k1) {
                 uint8_t *vt = v_ring + vs * L.tile_bytes;
@@ -528,7 +530,7 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
                 mma_commit(&s_full[t % SB]);
                 mma_commit(&k_empty[ks]);
                 if (++ks == NK) { ks = 0; kph ^= 1u; }
-                next_tile(tq, TP, p.B, ups);
+                next_tile<UC>(tq, TP, p.B, ups);
                 return true;
             };
             auto issue_pv = [&](int t) -> bool {
@@ -550,7 +552,7 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
                 mma_commit(&o_full[t % PB]);
                 mma_commit(&v_empty[vs]);
                 if (++vs == NV) { vs = 0; vph ^= 1u; }
-                next_tile(tp, TP, p.B, ups);
+                next_tile<UC>(tp, TP, p.B, ups);
                 return true;
             };
             // Q.K of tile q runs up to SB tiles ahead of P.V of tile v. With one query
@@ -605,7 +607,7 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
 #pragma unroll 1
         for (int lt = 0; lt <= ntiles && ok; ++lt) {
             const int h = ti.hr / p.RC, ids = idk;
-            if (lt < ntiles) next_tile(ti, TP, p.B, ups);
+            if (lt < ntiles) next_tile<UC>(ti, TP, p.B, ups);
             if (lt + 1 < ntiles) idk = page_ids();  // in flight while this tile waits for its slots
             if (lt < ntiles) ok = load(0, ids, h);
             if (lt > 0 && ok) ok = load(1, idv, hv);
@@ -709,8 +711,8 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
             if (!wg_sync()) return false;
             const int fh = uhr / p.RC, frc = uhr - fh * p.RC;
             const int frows = min(p.rows_unit, p.R - frc * p.rows_unit) - col0;  // of this warpgroup's columns
-            const int Tb = real_tiles(TP[ub + 1] - TP[ub]);
-            const int tpre = ups * TP[ub] + uhr * (Tb + UNIT_COST);  // the unit's first position
+            const int Tb = real_tiles<UC>(TP[ub + 1] - TP[ub]);
+            const int tpre = ups * TP[ub] + uhr * (Tb + UC);  // the unit's first position
             const bool to_slot = (tpre + Tb - 1) / W != tpre / W;
             float *slot = p.ws_partial + (size_t)(ub * ups + uhr + seg) * slot_floats;
             if (ell < CW) {
@@ -811,7 +813,7 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
                     if (ok) ok = wg_sync();
                 }
             }
-            next_tile(tnext, TP, p.B, ups);
+            next_tile<UC>(tnext, TP, p.B, ups);
             // the page's scales: K's in the exponent's unit, V's
             const int sslot = lt / SC_BATCH % SC_RING;
             if (ok) ok = wait_w(&sc_full[sslot], lt / (SC_BATCH * SC_RING) & 1);
@@ -862,7 +864,9 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
             if (lt >= PB && ok) ok = wait_w(&o_full[pb], ((lt - PB) / PB) & 1);  // P is free
             const bool fresh = first;
             bool raise = first, leave = false;
-            while (true) {
+            // the second raise in a row cannot come: the maxima are the tile's own then
+#pragma unroll 1
+            for (int tries = 0;; ++tries) {
                 if (!raise) {
                     __half2 top2 = __float2half2_rn(0.f);
                     if (ok) {
@@ -870,8 +874,8 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
                         for (int c0 = 0; c0 < CW; c0 += CH) {
                             float x[CH], l[CH];
                             tmem_load<CH>(saddr + c0, x);
-                            tmem_load<CH>(tm_l + c0, l);
                             tmem_wait_ld();
+                            tmem_load<CH>(tm_l + c0, l);
                             // in phases over the chunk, so that no value waits for the one before
                             uint64_t w[CH / 2];
                             uint32_t h[CH / 2], piece[3][CH / 4];
@@ -888,6 +892,7 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
                                 unpack2(w[i], a, b);
                                 w[i] = pack2(ex2_approx(a), ex2_approx(b));
                             }
+                            tmem_wait_ld();
 #pragma unroll
                             for (int i = 0; i < CH / 2; ++i) {
                                 float a, b;
@@ -922,7 +927,7 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
                         }
                         tmem_wait_st();
                     }
-                    raise = wg_any(1 + wg, !ok || !__hble2(top2, __float2half2_rn(P_MAX)));
+                    raise = wg_any(1 + wg, !ok || (tries < 2 && !__hble2(top2, __float2half2_rn(P_MAX))));
                     if (!raise) break;
                 }
                 if ((leave = wg_any(1 + wg, !ok))) break;
@@ -991,7 +996,7 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
                 // the next unit's query rows; the buffer's last products are those of the unit before this one
                 TileInfo nu = ti;
                 nu.j = nu.Tb - 1;
-                next_tile(nu, TP, p.B, ups);
+                next_tile<UC>(nu, TP, p.B, ups);
                 cut_queries(nu, lu + 1);
             }
         }
@@ -1039,7 +1044,7 @@ cudaError_t launch_q8(Q8Params &P, cudaStream_t stream) {
     const int sms = P.a.num_ctas;
     P.a.num_ctas = sms * S::NT;
     e = launch_programmatic(kfn, dim3(sms), dim3(S::THREADS), smem, stream, P);
-    return e != cudaSuccess ? e : launch_combine(P.a, stream);
+    return e != cudaSuccess ? e : launch_combine<UC>(P.a, stream);
 }
 
 template <int D>

@@ -52,6 +52,7 @@ constexpr int TILE_KEYS = 128;
 // fewer tiles. A unit occupies Tb + UNIT_COST positions of the schedule; the
 // last UNIT_COST hold no work.
 constexpr int UNIT_COST = 2;
+constexpr int UNIT_COST_Q8 = 4;    // of the 8-bit cache's kernel, whose tiles take half as long
 constexpr int PAGE = 16;
 constexpr int ROWS_MAX = 96;       // query rows (N*G) one unit carries
 constexpr int MAX_SEQS = 512;

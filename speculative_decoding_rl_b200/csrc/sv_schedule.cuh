@@ -28,18 +28,22 @@ SV_DEV int seq_tiles(const AttnParams &p, int b) {
     return ok ? (C + TILE_KEYS - 1) / TILE_KEYS : 0;
 }
 
-// Schedule positions of one unit of sequence b: its tiles plus UNIT_COST.
+// Schedule positions of one unit of sequence b: its tiles plus the unit's cost
+// UC (here and below; the same in every kernel of a call).
+template <int UC = UNIT_COST>
 SV_DEV int seq_slots(const AttnParams &p, int b) {
     const int t = seq_tiles(p, b);
-    return t > 0 ? t + UNIT_COST : 0;
+    return t > 0 ? t + UC : 0;
 }
 
 // Tiles of a sequence from its schedule positions.
-SV_DEV int real_tiles(int positions) { return positions > 0 ? positions - UNIT_COST : 0; }
+template <int UC = UNIT_COST>
+SV_DEV int real_tiles(int positions) { return positions > 0 ? positions - UC : 0; }
 
 // Exclusive prefix of per-sequence schedule positions (seq_slots) into
 // TP[0..B] (and, when CL is given, the context lengths into CL[0..B)); the
 // whole block participates.
+template <int UC = UNIT_COST>
 SV_DEV void tile_prefix(const AttnParams &p, int *TP, int *scratch, int *CL = nullptr) {
     const int nt = blockDim.x, tid = threadIdx.x;
     const int per = (p.B + nt - 1) / nt;
@@ -47,7 +51,7 @@ SV_DEV void tile_prefix(const AttnParams &p, int *TP, int *scratch, int *CL = nu
     int local = 0;
 #pragma unroll 1
     for (int b = s0; b < s1; ++b) {
-        local += seq_slots(p, b);
+        local += seq_slots<UC>(p, b);
         if (CL) CL[b] = p.ctx_lens[b];
     }
     const int lane = tid & 31, warp = tid >> 5;
@@ -66,7 +70,7 @@ SV_DEV void tile_prefix(const AttnParams &p, int *TP, int *scratch, int *CL = nu
 #pragma unroll 1
     for (int b = s0; b < s1; ++b) {
         TP[b] = run;
-        run += seq_slots(p, b);
+        run += seq_slots<UC>(p, b);
     }
     if (tid == nt - 1) TP[p.B] = run;
     __syncthreads();
@@ -96,6 +100,7 @@ struct TileInfo {
 // The tile after ti in the end-to-end order (j, then head/row chunk, then
 // sequence; sequences without tiles are skipped). Callers stop at their range's
 // end, so running past the last sequence only has to be harmless.
+template <int UC = UNIT_COST>
 SV_DEV void next_tile(TileInfo &ti, const int *TP, int B, int ups) {
     if (++ti.j < ti.Tb) return;
     ti.j = 0;
@@ -104,12 +109,13 @@ SV_DEV void next_tile(TileInfo &ti, const int *TP, int B, int ups) {
 #pragma unroll 1
     do {
         ++ti.b;
-        ti.Tb = ti.b < B ? real_tiles(TP[ti.b + 1] - TP[ti.b]) : 1;
+        ti.Tb = ti.b < B ? real_tiles<UC>(TP[ti.b + 1] - TP[ti.b]) : 1;
     } while (ti.b < B && ti.Tb == 0);
 }
 
 // The first tile a CTA owns and how many it owns: the tiles whose schedule
 // positions fall in [v0, v1) (positions past a unit's tiles hold no work).
+template <int UC = UNIT_COST>
 SV_DEV TileInfo cta_tiles(const int *TP, int B, int ups, int v0, int v1, int *ntiles) {
     TileInfo ti{0, 0, 0, 1};
     *ntiles = 0;
@@ -119,21 +125,21 @@ SV_DEV TileInfo cta_tiles(const int *TP, int B, int ups, int v0, int v1, int *nt
     const int off = v0 - ups * TP[ti.b];
     ti.hr = off / T1;
     ti.j = off - ti.hr * T1;
-    ti.Tb = real_tiles(T1);
+    ti.Tb = real_tiles<UC>(T1);
     if (ti.j >= ti.Tb) {  // a position past the unit's tiles: start at the next unit
         ti.j = ti.Tb - 1;
-        next_tile(ti, TP, B, ups);
+        next_tile<UC>(ti, TP, B, ups);
     }
     TileInfo w = ti;
     int n = 0;
 #pragma unroll 1
     while (w.b < B) {
-        const int pos = ups * TP[w.b] + w.hr * (w.Tb + UNIT_COST) + w.j;
+        const int pos = ups * TP[w.b] + w.hr * (w.Tb + UC) + w.j;
         if (pos >= v1) break;
         const int here = min(w.Tb - w.j, v1 - pos);
         n += here;
         w.j = w.Tb - 1;
-        next_tile(w, TP, B, ups);
+        next_tile<UC>(w, TP, B, ups);
     }
     *ntiles = n;
     return ti;
@@ -147,7 +153,8 @@ constexpr int SMEM_LIMIT = 227 * 1024;
 // The driver's tensor-map encoder, or null.
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 
-// Merges the partials of the units that were split over several CTAs into p.out.
+// Merges the partials of the units that were split over several ranges into p.out.
+template <int UC = UNIT_COST>
 cudaError_t launch_combine(const AttnParams &p, cudaStream_t stream);
 
 // Launch with programmatic stream serialization: the kernel may start while the
