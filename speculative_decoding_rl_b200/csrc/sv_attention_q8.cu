@@ -53,15 +53,15 @@ using namespace tc;
 namespace {
 
 // Shape of the kernel for RP padded rows per unit.
-template <int D, int RP>
+template <int RP>
 struct Q8Shape {
     static constexpr int CW = RP >= 64 ? 32 : RP;              // row columns per warpgroup
     static constexpr int NG = RP / CW;                         // warpgroups per range
     static constexpr int CH = CW % 16 ? 8 : 16;                // columns taken at a time
-    static constexpr int NT = RP == 96 ? 1 : D == 128 ? 2 : RP == 16 ? 4 : RP == 32 ? 3 : 2;  // ranges
+    static constexpr int NT = RP == 96 ? 1 : 2;                // ranges
     // O accumulators side by side: P's pieces enter a product's N together as far
     // as TMEM has room for their sums, the last one goes into the last sum.
-    static constexpr int ACC = RP == 64 ? 1 : RP >= 48 || NT == 3 ? 2 : 3;
+    static constexpr int ACC = RP == 64 ? 1 : RP >= 48 ? 2 : 3;
     static constexpr int SB = 2;                  // S buffers per range
     static constexpr int PB = NT == 1 ? 2 : 1;    // P buffers per range
     static constexpr int NQ = RP == 64 ? 1 : 2;   // query buffers per range
@@ -89,7 +89,7 @@ constexpr int MAX_RING = 16;   // K and V slots of a range at most
 constexpr float P_SCALE = 128.f, P_UNSCALE = 1.f / 128.f, P_MAX = 32768.f;
 // A range is at least this long: on small calls, shorter ranges would cost the
 // combine more partials than they save.
-constexpr int MIN_WIDTH = 2;
+constexpr int MIN_WIDTH = 4;
 
 struct Q8Layout {
     uint32_t tile_bytes, off_k, off_q, q_bytes, off_p, p_bytes, off_bar, off_tp, off_cl, off_red, off_nm, off_as,
@@ -98,7 +98,7 @@ struct Q8Layout {
 
 template <int D, int RP>
 __host__ __device__ inline Q8Layout q8_layout(int NK, int NV, int B) {
-    using S = Q8Shape<D, RP>;
+    using S = Q8Shape<RP>;
     Q8Layout L;
     L.tile_bytes = (uint32_t)TILE_KEYS * D;
     L.off_k = S::NT * NV * L.tile_bytes;           // [range][NV]
@@ -107,7 +107,7 @@ __host__ __device__ inline Q8Layout q8_layout(int NK, int NV, int B) {
     L.off_p = L.off_q + S::NT * S::NQ * L.q_bytes;
     L.p_bytes = 3u * RP * TILE_KEYS;               // [range][PB]: three pieces
     L.off_bar = L.off_p + S::NT * S::PB * L.p_bytes;
-    const int nbar = S::NT * (2 * NK + 3 * NV + S::NQ + 2 * S::SB + 2 * S::PB + 1 + 2 * SC_RING) + S::WGS;
+    const int nbar = S::NT * (2 * NK + 3 * NV + S::NQ + 2 * S::SB + 2 * S::PB + 1 + 2 * SC_RING);
     L.off_tp = L.off_bar + 8u * nbar;
     L.off_cl = L.off_tp + 4u * (B + 1);
     L.off_red = (L.off_cl + 4u * B + 15u) & ~15u;
@@ -183,22 +183,23 @@ SV_DEV void cut_query_row(uint8_t *a, uint8_t *b, float *scale, int lane) {
     if (lane % 16 == 0) *scale = finite ? exp2_int(e) : NAN;
 }
 
-// Sums of CH (8 or 16) values over the warp's lanes: the lane returns that of
-// value lane / (32 / CH). Each step halves the values a lane carries: 16 shuffles
-// in place of 80 for 16 values.
-template <int CH>
-SV_DEV float warp_sums(float *v, int lane) {
+// Sums (or maxima) of CH (8 or 16) values over the warp's lanes: the lane returns
+// that of value lane / (32 / CH). Each step halves the values a lane carries: 16
+// shuffles in place of 80 for 16 values.
+template <int CH, bool MAX = false>
+SV_DEV float warp_reduce(float *v, int lane) {
+    auto join = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
 #pragma unroll
     for (int half = CH / 2, bit = 16; half > 0; half >>= 1, bit >>= 1) {
         const bool up = lane & bit;
 #pragma unroll
         for (int i = 0; i < half; ++i) {
             const float send = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
+            v[i] = join(keep, __shfl_xor_sync(0xffffffffu, send, bit));
         }
     }
 #pragma unroll
-    for (int bit = 16 / CH; bit > 0; bit >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], bit);
+    for (int bit = 16 / CH; bit > 0; bit >>= 1) v[0] = join(v[0], __shfl_xor_sync(0xffffffffu, v[0], bit));
     return v[0];
 }
 
@@ -265,7 +266,8 @@ SV_DEV bool wait_phase(uint64_t *b, uint32_t parity, volatile int *abort) {
     return done;
 }
 
-// Barrier of the 128 threads of a warpgroup with the or of a predicate.
+// Barrier of the 128 threads of a warpgroup, plain and with the or of a predicate.
+SV_DEV void wg_sync(int id) { named_bar_sync(id, 128); }
 SV_DEV bool wg_any(int id, bool v) {
     uint32_t r;
     asm volatile(
@@ -280,8 +282,8 @@ SV_DEV bool wg_any(int id, bool v) {
 }
 
 template <int D, int RP>
-__global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(const __grid_constant__ Q8Params P) {
-    using S = Q8Shape<D, RP>;
+__global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const __grid_constant__ Q8Params P) {
+    using S = Q8Shape<RP>;
     constexpr int CW = S::CW, NG = S::NG, NT = S::NT, SB = S::SB, PB = S::PB, NQ = S::NQ, CH = S::CH;
     constexpr int ACC = S::ACC;
     constexpr int MATH_WARPS = S::MATH_WARPS, NTHREADS = S::THREADS;
@@ -308,7 +310,6 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
     uint64_t *o_full = p_full + PB;     // [PB] the tile's PV has completed, its P is free
     uint64_t *sc_full = o_full + PB, *sc_empty = sc_full + SC_RING;
     uint64_t *done_bar = sc_empty + SC_RING;
-    uint64_t *wg_bar = bar + NT * nrb + (warp >> 2);
     int *TP = reinterpret_cast<int *>(base + L.off_tp);
     int *CL = reinterpret_cast<int *>(base + L.off_cl);
     int *rowi = reinterpret_cast<int *>(base + L.off_rowi);      // [RP] row r -> r / G
@@ -331,7 +332,6 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
         for (int i = 0; i < PB; ++i) { mbar_init(&p_full[i], 4 * NG); mbar_init(&o_full[i], 1); }
         for (int i = 0; i < SC_RING; ++i) { mbar_init(&sc_full[i], 1); mbar_init(&sc_empty[i], 4 * NG); }
         mbar_init(done_bar, 1);
-        for (int g = 0; g < NG; ++g) mbar_init(bar + NT * nrb + r * NG + g, 4);
         if (r == 0) *abort_flag = 0;
         fence_barrier_init();
     }
@@ -625,8 +625,8 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
     } else {
         // ------------------------------ softmax ------------------------------
         // A wait that runs out leaves `ok` false; the warp goes on to the next vote
-        // without work, and the warpgroup leaves together from there, so that no
-        // warp is missing at a barrier.
+        // without work, past every barrier on the way, and the warpgroup leaves
+        // together from there, so that no warp is missing at a barrier.
         const int wg = warp >> 2, cg = wg - r * NG;
         const int wiw = warp & 3;          // warp within the warpgroup = TMEM lane quadrant
         const int ell = wiw * 32 + lane;   // key (S) / head dim (O) lane
@@ -641,19 +641,12 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
         uint64_t *umask = reinterpret_cast<uint64_t *>(base + L.off_umask) + wg * 64;
         float *qs_ring = reinterpret_cast<float *>(base + L.off_qs) + r * QS_RING * RP;
         const size_t slot_floats = slot_stride(p.rows_unit, D);
-        uint32_t wg_phase = 0;
         bool ok = true;
         int lu = -1, ub = 0, uhr = 0, uC = 0;
 
         auto warp_arrive = [&](uint64_t *b) {
             __syncwarp();
             if (lane == 0) mbar_arrive(b);
-        };
-        auto wg_sync = [&]() -> bool {
-            warp_arrive(wg_bar);
-            const bool done = wait_w(wg_bar, wg_phase);
-            wg_phase ^= 1;
-            return done;
         };
         // this warpgroup's share of the query rows of tile ti's unit, the range's u-th
         auto cut_queries = [&](const TileInfo &ti, int u) {
@@ -705,10 +698,10 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
                 float l[CH];
                 tmem_load<CH>(tm_l + c0, l);
                 tmem_wait_ld();
-                const float v = warp_sums<CH>(l, lane);
+                const float v = warp_reduce<CH>(l, lane);
                 if (lane % (32 / CH) == 0) red[wiw * RP + c0 + lane / (32 / CH)] = v;
             }
-            if (!wg_sync()) return false;
+            wg_sync(1 + wg);
             const int fh = uhr / p.RC, frc = uhr - fh * p.RC;
             const int frows = min(p.rows_unit, p.R - frc * p.rows_unit) - col0;  // of this warpgroup's columns
             const int Tb = real_tiles<UC>(TP[ub + 1] - TP[ub]);
@@ -724,7 +717,8 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
                     slot[(size_t)p.rows_unit * D + p.rows_unit + col0 + ell] = l;
                 }
             }
-            if (!wg_sync() || !wait_w(&o_full[tlast % PB], (tlast / PB) & 1)) return false;
+            wg_sync(1 + wg);
+            if (!wait_w(&o_full[tlast % PB], (tlast / PB) & 1)) return false;
             tc_fence_after();
             const bool marked = vnan[lu % UNIT_RING] != 0;
             uint16_t *ounit = p.out + (((size_t)ub * p.N + frc * P.Nc) * p.Hq + fh * p.G) * D + ell;
@@ -800,7 +794,10 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
             const TileInfo ti = tnext;
             const bool first = lt == 0 || end || ti.j == 0;
             if (first) {
-                if (lt > 0 && ok) ok = finish_unit(lt - 1);
+                if (lt > 0) {
+                    if (wg_any(1 + wg, !ok)) break;
+                    ok = finish_unit(lt - 1);
+                }
                 if (end) break;
                 ++lu;
                 ub = ti.b;
@@ -810,7 +807,7 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
                 if (p.mask) {
 #pragma unroll 1
                     for (int k = ell; k < p.N; k += 128) umask[k] = __ldg(p.mask + (size_t)ub * p.N + k);
-                    if (ok) ok = wg_sync();
+                    wg_sync(1 + wg);
                 }
             }
             next_tile<UC>(tnext, TP, p.B, ups);
@@ -934,27 +931,23 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
                 // tile column maxima over the 128 keys; this tile's weights out of the row sums
 #pragma unroll 1
                 for (int c0 = 0; c0 < CW; c0 += CH) {
-                    float y[CH], l[CH], mine = 0.f;
+                    float y[CH], l[CH];
                     tmem_load<CH>(saddr + c0, y);
                     if (!fresh) tmem_load<CH>(tm_l + c0, l);
-                    else
-#pragma unroll
-                        for (int c = 0; c < CH; ++c) l[c] = 0.f;
                     tmem_wait_ld();
 #pragma unroll
                     for (int c = 0; c < CH; ++c) {
-                        const float e = y[c] * ks1;
-                        float m;
-                        asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(fmaf(e, qs[c0 + c], lv)));
-                        if (lane == c) mine = m;
+                        const float e = y[c] * ks1, q = qs[c0 + c];
                         // a sum that overflowed held nothing that counts beside the weight that made it so
-                        if (!fresh) l[c] = l[c] == INFINITY ? 0.f : l[c] - ex2_approx(fmaf(e, qs[c0 + c], nm[c0 + c]));
+                        l[c] = fresh || l[c] == INFINITY ? 0.f : l[c] - ex2_approx(fmaf(e, q, nm[c0 + c]));
+                        y[c] = fmaf(e, q, lv);
                     }
                     tmem_store<CH>(tm_l + c0, l);
-                    if (lane < CH) red[wiw * RP + c0 + lane] = mine;
+                    const float m = warp_reduce<CH, true>(y, lane);
+                    if (lane % (32 / CH) == 0) red[wiw * RP + c0 + lane / (32 / CH)] = m;
                 }
                 tmem_wait_st();
-                ok = wg_sync();
+                wg_sync(1 + wg);
                 if (ell < CW) {
                     const float m_old = fresh ? M_NONE : -nm[ell];
                     const float rmax = fmaxf(fmaxf(red[ell], red[RP + ell]), fmaxf(red[2 * RP + ell], red[3 * RP + ell]));
@@ -962,7 +955,7 @@ __global__ void __launch_bounds__(Q8Shape<D, RP>::THREADS, 1) attn_q8_kernel(con
                     nm[ell] = -mx;
                     as[ell] = ex2_approx(m_old - mx);  // M_NONE - finite underflows to 0
                 }
-                if (ok) ok = wg_sync();
+                wg_sync(1 + wg);
                 if (!fresh) {
                     // the row sums and O^T's columns follow, once the previous tile's PV has landed
                     if (ok) ok = wait_w(&o_full[(lt - 1) % PB], ((lt - 1) / PB) & 1);
@@ -1030,7 +1023,7 @@ bool encode_pool_q8(CUtensorMap *m, const void *pool, int num_blocks, int Hkv, i
 
 template <int D, int RP>
 cudaError_t launch_q8(Q8Params &P, cudaStream_t stream) {
-    using S = Q8Shape<D, RP>;
+    using S = Q8Shape<RP>;
     // as many K and V slots as fit, V's the larger half (its slots are held longer)
     int slots = MAX_RING;
     while (q8_layout<D, RP>(slots / 2, slots - slots / 2, P.a.B).total + 1024 > (uint32_t)SMEM_LIMIT)
@@ -1062,7 +1055,7 @@ cudaError_t launch_q8_rp(Q8Params &P, int RP, cudaStream_t stream) {
 }  // namespace
 
 size_t attention_q8_workspace_bytes(int B, int N, int Hq, int Hkv, int D, int num_ctas) {
-    return attention_workspace_bytes(B, N, Hq, Hkv, D, num_ctas * Q8Shape<64, 16>::NT);
+    return attention_workspace_bytes(B, N, Hq, Hkv, D, num_ctas * Q8Shape<16>::NT);
 }
 
 cudaError_t launch_attention_q8(const AttnParams &p, const float *scales, cudaStream_t stream) {
