@@ -374,7 +374,12 @@ SV_API sv_status sv_kv_append_q8(const sv_attn_desc *desc, const sv_rope_desc *r
 
 /* sv_verify_attention over the 8-bit cache: same arguments, masks, limits and
  * flags (q and out bf16; the pools 16-byte aligned, scales 8-byte aligned).
- * A page with a block id outside the pool reads as zeros. */
+ * A page with a block id outside the pool reads as zeros. Scores and sums are
+ * fp32; q is used to 2^-18 of its row's largest entry, a key's weight to 2^-9 of
+ * itself and, far below the row's largest, to 2^-24 of that. A NaN entry of K
+ * makes NaN of the rows that see its key, of V that entry of theirs; a row of q
+ * with an entry that is not finite gives NaN. Rows that do not see a key are not
+ * touched by what it holds. */
 SV_API size_t sv_verify_attention_q8_workspace_size(const sv_attn_desc *desc);
 
 SV_API sv_status sv_verify_attention_q8(const sv_attn_desc *desc, const void *q, const sv_kv_q8 *kv,

@@ -14,6 +14,9 @@
 // Little is computed; what bounds a call is memory when there are many rows, and
 // the chain of loads (length, then block id and positions, then cosines and
 // sines) when there are few, so the rows themselves are asked for first.
+// Measured: 256 x 9 rows of 40 + 16 heads of 128 (67 MB) 13.3 us with L2 warm,
+// 18.8 us cold (0.54 of the copy rate); 16 ragged prompts of up to 1500 rows into
+// the 8-bit cache (259 MB) 75.8 us (0.52); 5 rows of one sequence 3.1 us.
 #include "sv_page8.cuh"
 #include "sv_q8.h"
 
