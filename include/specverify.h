@@ -373,7 +373,8 @@ SV_API sv_status sv_kv_append_q8(const sv_attn_desc *desc, const sv_rope_desc *r
                                  void *q_out, int32_t *status_flags, void *stream);
 
 /* sv_verify_attention over the 8-bit cache: same arguments, masks, limits and
- * flags (q and out bf16; the pools 16-byte aligned, scales 8-byte aligned).
+ * flags (q and out bf16; the pools 16-byte aligned, scales 8-byte aligned; out,
+ * workspace and status_flags must not overlap an input or one another).
  * A page with a block id outside the pool reads as zeros. Scores and sums are
  * fp32; q is used to 2^-18 of its row's largest entry, a key's weight to 2^-9 of
  * itself and, far below the row's largest, to 2^-24 of that. A NaN entry of K
@@ -388,7 +389,7 @@ SV_API sv_status sv_verify_attention_q8(const sv_attn_desc *desc, const void *q,
                                         size_t workspace_bytes, int32_t *status_flags, void *stream);
 
 /* sv_kv_commit over the 8-bit cache: same arguments, rules and flags, D in
- * {64, 128}. Pages that receive a row are written back under the scale of the
+ * {64, 128}; every layer's pools and scales are its own. Pages that receive a row are written back under the scale of the
  * rows they keep; where nothing moves nothing is written. */
 SV_API sv_status sv_kv_commit_q8(const sv_attn_desc *desc, int32_t num_layers, const sv_kv_q8 *layers,
                                  const int32_t *block_table, const int32_t *ctx_lens, const int32_t *accept_len,

@@ -364,9 +364,10 @@ def make_new_rows(q, k, v, positions=None, new_lens=None) -> SvNewRows:
 def make_kv_q8(k_pool, v_pool, scales) -> SvKVQ8:
     """One layer of the 8-bit cache: e4m3 pools [num_blocks][Hkv][16][D], fp32 scales [num_blocks][Hkv][2]
     (tensors, kept alive on the returned object, or device addresses)."""
-    for x, name in ((k_pool, "torch.float8_e4m3fn"), (v_pool, "torch.float8_e4m3fn"), (scales, "torch.float32")):
-        if hasattr(x, "dtype") and (str(x.dtype) != name or not x.is_contiguous()):
-            raise ValueError(f"expected a contiguous {name} tensor, got {x.dtype}")
+    import torch
+    for x, dtype in ((k_pool, torch.float8_e4m3fn), (v_pool, torch.float8_e4m3fn), (scales, torch.float32)):
+        if isinstance(x, torch.Tensor) and (x.dtype != dtype or not x.is_contiguous()):
+            raise ValueError(f"expected a contiguous {dtype} tensor, got {x.dtype}")
     d = SvKVQ8(_ptr(k_pool), _ptr(v_pool), _ptr(scales))
     d._keep = (k_pool, v_pool, scales)
     return d

@@ -516,6 +516,24 @@ sv_status sv_verify_attention_q8(const sv_attn_desc *d, const void *q, const sv_
     if ((s = check_q8(kv)) != SV_OK) return s;
     const sv_paged_kv pools = {kv->k_pool, kv->v_pool};
     if ((s = check_attn_ptrs(q, &pools, block_table, ctx_lens, draft_mask, out, status_flags)) != SV_OK) return s;
+    {
+        // units are read and written in any order: no output over an input or another output
+        const size_t rows = (size_t)d->num_seqs * d->num_q_rows, B4 = (size_t)d->num_seqs * 4;
+        const size_t heads = (size_t)d->num_blocks * d->num_kv_heads, io = rows * d->num_q_heads * d->head_dim * 2;
+        const size_t pool = heads * sv::PAGE * d->head_dim;
+        const void *o[] = {out, workspace, status_flags};
+        const size_t ob[] = {io, workspace_bytes, B4};
+        const void *in[] = {q, kv->k_pool, kv->v_pool, kv->scales, block_table, ctx_lens, draft_mask};
+        const size_t ib[] = {io, pool, pool, heads * 8, B4 * (size_t)d->max_blocks_per_seq, B4, rows * 8};
+        for (int i = 0; i < 3; ++i) {
+            for (int j = 0; j < 7; ++j)
+                if (overlaps(o[i], ob[i], in[j], ib[j]))
+                    return fail(SV_ERR_INVALID_ARG, "out, workspace and status_flags must not overlap an input");
+            for (int j = 0; j < i; ++j)
+                if (overlaps(o[i], ob[i], o[j], ob[j]))
+                    return fail(SV_ERR_INVALID_ARG, "out, workspace and status_flags must not overlap");
+        }
+    }
     const int ctas = sv::attention_num_ctas();
     if (ctas <= 0) return fail(SV_ERR_CUDA, "cannot query the current device");
     const size_t need = sv::attention_q8_workspace_bytes(d->num_seqs, d->num_q_rows, d->num_q_heads,

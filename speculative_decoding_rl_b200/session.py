@@ -115,6 +115,28 @@ class CommitCall:
         return self.new_ctx_lens
 
 
+def _expect(x, name: str, shape, dtype) -> None:
+    """The library reads plain contiguous arrays: refuse anything else before its address is taken."""
+    if tuple(x.shape) != tuple(shape) or x.dtype != dtype or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, got {x.dtype} "
+                         f"{tuple(x.shape)} with strides {tuple(x.stride())}")
+
+
+def _expect_cache(desc, kv, q8: bool) -> None:
+    pool = (desc.num_blocks, desc.num_kv_heads, desc.block_size, desc.head_dim)
+    if len(kv) != (3 if q8 else 2):
+        raise ValueError("a layer's cache is (k_pool, v_pool, scales)" if q8 else "a layer's cache is (k_pool, v_pool)")
+    for x, name in zip(kv, ("k_pool", "v_pool")):
+        _expect(x, name, pool, torch.float8_e4m3fn if q8 else torch.bfloat16)
+    if q8:
+        _expect(kv[2], "scales", (*pool[:2], 2), torch.float32)
+
+
+def _expect_lengths(desc, block_table, ctx_lens) -> None:
+    _expect(block_table, "block_table", (desc.num_seqs, desc.max_blocks_per_seq), torch.int32)
+    _expect(ctx_lens, "ctx_lens", (desc.num_seqs,), torch.int32)
+
+
 class AppendCall:
     """Rotate the new rows and write them to a layer's bf16 cache (arguments prepared once).
 
@@ -126,9 +148,15 @@ class AppendCall:
 
     def __init__(self, desc, rope, kv, block_table, ctx_lens, q, k, v, positions=None, new_lens=None,
                  q_out: Optional[torch.Tensor] = None):
+        if q is None and q_out is not None:
+            raise ValueError("q and q_out go together")
         if tuple(k.shape) != (desc.num_seqs, desc.num_q_rows, desc.num_kv_heads, desc.head_dim) or \
                 (q is not None and q.shape[2] != desc.num_q_heads):
             raise ValueError("the new rows' shapes do not match the descriptor")
+        _expect_cache(desc, kv, self._entry == "sv_kv_append_q8")
+        _expect_lengths(desc, block_table, ctx_lens)
+        if q_out is not None:
+            _expect(q_out, "q_out", (desc.num_seqs, desc.num_q_rows, desc.num_q_heads, desc.head_dim), torch.bfloat16)
         self.desc, self.rope = desc, rope
         self.rows = make_new_rows(q, k, v, positions, new_lens)
         self.pools, self.kv = kv, self._cache(kv)
@@ -163,6 +191,14 @@ class AttentionQ8Call:
     """Verify attention over a layer's 8-bit cache; kv: (k_pool, v_pool, scales), q bf16 [B][N][Hq][D]."""
 
     def __init__(self, desc, kv, block_table, ctx_lens, q, draft_mask=None, out: Optional[torch.Tensor] = None):
+        rows = (desc.num_seqs, desc.num_q_rows, desc.num_q_heads, desc.head_dim)
+        _expect_cache(desc, kv, True)
+        _expect_lengths(desc, block_table, ctx_lens)
+        _expect(q, "q", rows, torch.bfloat16)
+        if out is not None:
+            _expect(out, "out", rows, torch.bfloat16)
+        if draft_mask is not None:
+            _expect(draft_mask, "draft_mask", rows[:2], torch.int64)
         self.desc = desc
         self.pools, self.kv = kv, make_kv_q8(*kv)
         self.block_table, self.ctx_lens, self.q, self.mask = block_table, ctx_lens, q, draft_mask
@@ -180,9 +216,15 @@ class AttentionQ8Call:
 
 
 class CommitQ8Call:
-    """KV commit after accept over the 8-bit caches of all layers; layers: (k_pool, v_pool, scales) each."""
+    """KV commit after accept over the 8-bit caches of all layers; layers: (k_pool, v_pool, scales) each, accept_path
+    [B][N-1] (one column for N = 1)."""
 
     def __init__(self, desc, layers, block_table, ctx_lens, accept_len, accept_path):
+        for layer in layers:
+            _expect_cache(desc, layer, True)
+        _expect_lengths(desc, block_table, ctx_lens)
+        _expect(accept_len, "accept_len", (desc.num_seqs,), torch.int32)
+        _expect(accept_path, "accept_path", (desc.num_seqs, max(desc.num_q_rows - 1, 1)), torch.int32)
         self.desc, self.layers = desc, layers
         self.block_table, self.ctx_lens = block_table, ctx_lens
         self.accept_len, self.accept_path = accept_len, accept_path

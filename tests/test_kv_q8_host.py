@@ -177,6 +177,52 @@ def test_row_strides_of_fused_projections():
     assert sv.make_rope_desc(None).rotary_dim == 0
 
 
+def test_attention_q8_refuses_outputs_over_inputs():
+    ws, need = 0x100000000, 1 << 20
+    for kw in (dict(out=Q), dict(out=Q + 20464), dict(out=KP), dict(ws=VP), dict(out=ws + 256), dict(status=CL + 4),
+               dict(status=TB), dict(ws=0x100000000, out=0x100000000 + need - 16)):
+        a = {**dict(out=QO, ws=ws, status=ST), **kw}
+        with pytest.raises(sv.SvError) as e:
+            sv.sv_verify_attention_q8(desc(), Q, sv.SvKVQ8(KP, VP, SC), TB, CL, None, a["out"], a["ws"], need,
+                                      a["status"], stream=0)
+        assert e.value.status == 1 and "overlap" in sv.sv_last_error()
+
+
+def test_call_objects_refuse_other_layouts():
+    from speculative_decoding_rl_b200.session import AppendCall, AppendQ8Call, AttentionQ8Call, CommitQ8Call
+    B, N, Hq, Hkv, D, mb, nb = 2, 3, 4, 2, 64, 4, 9
+    d = sv.SvAttnDesc(B, N, Hq, Hkv, D, 16, mb, nb)
+    f8 = torch.float8_e4m3fn
+    pool, sc = torch.zeros((nb, Hkv, 16, D)).to(f8), torch.zeros((nb, Hkv, 2))
+    wide = torch.zeros((B, mb + 1), dtype=torch.int32)
+    table, ctx = wide[:, :mb].contiguous(), torch.zeros(B, dtype=torch.int32)
+    q = torch.zeros((B, N, Hq, D), dtype=torch.bfloat16)
+    k = torch.zeros((B, N, Hkv, D), dtype=torch.bfloat16)
+    mask = torch.zeros((B, N), dtype=torch.int64)
+    kv, rope = (pool, pool, sc), sv.make_rope_desc(None)
+
+    def bad(call):
+        with pytest.raises(ValueError):
+            call()
+    for kv2 in ((pool, pool), (pool[:8], pool, sc), (pool, pool.float(), sc), (pool, pool, sc.double()),
+                (pool, pool, sc[..., :1]), (pool.transpose(1, 2), pool, sc)):
+        bad(lambda: AttentionQ8Call(d, kv2, table, ctx, q))
+        bad(lambda: AppendQ8Call(d, rope, kv2, table, ctx, q, k, k))
+        bad(lambda: CommitQ8Call(d, [kv, kv2], table, ctx, ctx, torch.zeros((B, N - 1), dtype=torch.int32)))
+    for t2, c2 in ((wide[:, :mb], ctx), (table.long(), ctx), (table, ctx.long()), (table, ctx[:1])):
+        bad(lambda: AttentionQ8Call(d, kv, t2, c2, q))
+        bad(lambda: AppendQ8Call(d, rope, kv, t2, c2, q, k, k))
+        bad(lambda: AppendCall(d, rope, (k, k), t2, c2, q, k, k))
+    bad(lambda: AttentionQ8Call(d, kv, table, ctx, q.float()))
+    bad(lambda: AttentionQ8Call(d, kv, table, ctx, q.transpose(1, 2)))
+    bad(lambda: AttentionQ8Call(d, kv, table, ctx, q, mask.int()))
+    bad(lambda: AttentionQ8Call(d, kv, table, ctx, q, out=q[:, :2]))
+    bad(lambda: AppendQ8Call(d, rope, kv, table, ctx, None, k, k, q_out=q))
+    bad(lambda: AppendQ8Call(d, rope, kv, table, ctx, q, k, k[:, :2]))
+    bad(lambda: CommitQ8Call(d, [kv], table, ctx, ctx, torch.zeros((B, N), dtype=torch.int32)))
+    bad(lambda: AttentionQ8Call(d, kv, table, ctx, q))  # all well but the device
+
+
 # ------------------------------------------------------------------ the plain forms themselves
 def test_page_exponent_is_the_smallest_that_holds():
     rng = np.random.default_rng(1)
