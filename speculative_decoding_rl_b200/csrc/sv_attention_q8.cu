@@ -10,7 +10,7 @@
 // pieces whose sum holds it:
 //   S^T = K Q^T  q, scaled by a power of two of its row, is the sum of two e4m3
 //                values: bf16 has 8 significant bits, e4m3 four, so the sum is
-//                exact down to 2^-18 of the row's largest entry. Two products
+//                exact down to 2^-17 of the row's largest entry. Two products
 //                over the same K accumulate into S.
 //   O^T = V^T P  the weights p, rounded to fp16, are cut into three e5m2 values
 //                (3 significant bits each, fp16's own exponent range): at least
@@ -258,10 +258,13 @@ SV_DEV uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-SV_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
+// The sums of a pair of products and the negated maxima, one at a time: two to an
+// instruction they would be contracted with the products.
+SV_DEV uint64_t sub_max(uint64_t x, uint64_t nm) {
+    float a, b, c, d;
+    unpack2(x, a, b);
+    unpack2(nm, c, d);
+    return pack2(__fadd_rn(a, c), __fadd_rn(b, d));
 }
 
 // Bounded wait on a phase, in few instructions (there are two dozen of them in
@@ -872,7 +875,7 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
             if (lt >= PB && ok) ok = wait_w(&o_full[pb], ((lt - PB) / PB) & 1);  // P is free
             const bool fresh = first;
             bool raise = first, leave = false;
-            // the second raise in a row cannot come: the maxima are the tile's own then
+            // a second raise in a row cannot come: the maxima are the tile's own then
 #pragma unroll 1
             for (int tries = 0;; ++tries) {
                 if (!raise) {
@@ -891,8 +894,10 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
                             for (int c4 = 0; c4 < CH / 4; ++c4) {
                                 const ulonglong2 q4 = reinterpret_cast<const ulonglong2 *>(qs + c0)[c4];
                                 const ulonglong2 m4 = reinterpret_cast<const ulonglong2 *>(nm + c0)[c4];
-                                w[2 * c4] = fma2(mul2(pack2(x[c4 * 4], x[c4 * 4 + 1]), ksc), q4.x, m4.x);
-                                w[2 * c4 + 1] = fma2(mul2(pack2(x[c4 * 4 + 2], x[c4 * 4 + 3]), ksc), q4.y, m4.y);
+                                // the product is rounded before the maximum, rounded alike, is taken off: the
+                                // largest score's exponent is then 0 however large it is
+                                w[2 * c4] = sub_max(mul2(mul2(pack2(x[c4 * 4], x[c4 * 4 + 1]), ksc), q4.x), m4.x);
+                                w[2 * c4 + 1] = sub_max(mul2(mul2(pack2(x[c4 * 4 + 2], x[c4 * 4 + 3]), ksc), q4.y), m4.y);
                             }
 #pragma unroll
                             for (int i = 0; i < CH / 2; ++i) {
@@ -950,8 +955,8 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
                     for (int c = 0; c < CH; ++c) {
                         const float e = y[c] * ks1, q = qs[c0 + c];
                         // a sum that overflowed held nothing that counts beside the weight that made it so
-                        l[c] = fresh || l[c] == INFINITY ? 0.f : l[c] - ex2_approx(fmaf(e, q, nm[c0 + c]));
-                        y[c] = fmaf(e, q, lv);
+                        l[c] = fresh || l[c] == INFINITY ? 0.f : l[c] - ex2_approx(__fadd_rn(__fmul_rn(e, q), nm[c0 + c]));
+                        y[c] = __fadd_ru(__fmul_rn(e, q), lv);  // no weight passes 1, however large the scores
                     }
                     tmem_store<CH>(tm_l + c0, l);
                     const float m = warp_reduce<CH, true>(y, lane);

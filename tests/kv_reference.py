@@ -148,11 +148,13 @@ def attend64(q, kv, table, ctx, mask=None):
     roundings can move each entry by.
 
     With w the softmax weights, A = sum w |v|: each weight enters the product with V rounded to at least 9 bits
-    (2^-9 of itself; half a step of a 3 x 3-bit expansion), its exponential adds 2^-20, and a score off by d moves it
-    by e^d - 1, and the sum it is divided by likewise: 2 (e^d - 1) in all. The score is a sum of D products, exact in
-    fp32 but for its additions (D roundings of at most 2^-23 of the sum of the magnitudes, an extra bit for adders
-    that cut off), of q held in two 4-bit pieces (exact down to 2^-19 of the row's largest entry). The output is
-    rounded to bf16 (2^-8 of itself)."""
+    (2^-9 of itself; half a step of a 3 x 3-bit expansion), or, where it is so small that the pieces' exponents end,
+    to half of e5m2's smallest step, 2^-17, on a scale on which the row's largest weight times V's scale is at least
+    2^7: 2^-24 of that largest. Its exponential adds 2^-20, and a score off by d moves it by e^d - 1, and the sum it is
+    divided by likewise: 2 (e^d - 1) in all. The score is a sum of D products, exact in fp32 but for its additions
+    (D roundings of at most 2^-23 of the sum of the magnitudes, an extra bit for adders that cut off), of q held in two
+    4-bit pieces on a scale on which its row's largest entry is above 224: off by at most half of e4m3's smallest step,
+    2^-10, which is less than 2^-17 of that entry. The output is rounded to bf16 (2^-8 of itself)."""
     k_pool, v_pool, scales = kv
     B, N, Hq, D = q.shape
     Hkv, nb = k_pool.shape[1], k_pool.shape[0]
@@ -194,11 +196,15 @@ def attend64(q, kv, table, ctx, mask=None):
                 o, A = w @ v[h], w @ v[h].abs()
             kk = k[h].abs().nan_to_num(0.0)
             d = ((qd.abs() @ kk.T) * D * 2.0 ** -22 +
-                 qd.abs().amax(1, keepdim=True) * kk.sum(-1) * 2.0 ** -19) / math.sqrt(D)
+                 qd.abs().amax(1, keepdim=True) * kk.sum(-1) * 2.0 ** -17) / math.sqrt(D)
             d = torch.where(seen, d, torch.zeros_like(d))
             d = d.amax(1, keepdim=True)
+            # the floor of a weight, in the units of the e4m3 values it multiplies
+            sv = torch.where(good[:, None], sc[:, h, 1:], torch.ones_like(sc[:, h, 1:])).repeat(1, PAGE).reshape(-1)[:C]
+            v8 = (v[h] / sv[:, None]).abs().nan_to_num(0.0)
+            floor = 2.0 ** -24 * (w * sv).amax(1, keepdim=True) * (seen.double() @ v8)
             out[b, :, hq] = o
-            tol[b, :, hq] = 2.0 ** -8 * o.abs() + (2.0 ** -9 + 2.0 ** -20 + 2 * torch.expm1(d)) * A * 1.01 + 1e-37
+            tol[b, :, hq] = 2.0 ** -8 * o.abs() + (2.0 ** -9 + 2.0 ** -20 + 2 * torch.expm1(d)) * A * 1.01 + floor + 1e-37
     return out, tol
 
 

@@ -276,6 +276,27 @@ def test_attention_sink_over_a_flat_tail(gap):
     check_attend(5, 8, 2, 128, [20000], seed=40, spoil=spoil)
 
 
+@pytest.mark.parametrize("size", [2.0 ** 10, 2.0 ** 22, 2.0 ** 40])
+@pytest.mark.parametrize("N,Hq,D", [(1, 4, 64), (5, 8, 128), (11, 16, 128)])
+def test_attention_huge_scores_pick_one_key(size, N, Hq, D):
+    # scores of `size` and more apart, to the end of what fp32 counts in: all weight on the largest
+    def spoil(q, kv, table, ctx, nb):
+        q.zero_()
+        q[..., 0] = size
+        kv[2][..., 0] = 1.0
+        kv[0][..., 0] = torch.randint(-20, 20, kv[0].shape[:3], generator=gen(3)).float().to(F8)
+        kv[0][table[0, 2], :, 9, 0] = 22.0
+        kv[0][table[1, 0], :, 3, 0] = 22.0
+    call, got, want, tol = run_attend(N, Hq, 2, D, [1500, 20], seed=47, spoil=spoil)
+    assert not call.status.any()
+    # exp(-2 * 2^10 / sqrt(D)) of the other keys is below 2^-180: the picked key's V, rounded once
+    v = [call.pools[1][call.block_table[b, p], :, r].cpu().double() *
+         call.pools[2][call.block_table[b, p], :, 1, None].cpu().double() for b, p, r in ((0, 2, 9), (1, 0, 3))]
+    for b in range(2):
+        pick = v[b].repeat_interleave(Hq // 2, 0)[None].expand(N, Hq, D)
+        assert ((got[b] - pick).abs() <= (2.0 ** -8 + 2.0 ** -9) * pick.abs()).all()
+
+
 def test_attention_rows_of_unlike_size():
     # a row's precision is its own, whatever the size of its neighbours
     def spoil(q, kv, table, ctx, nb):
