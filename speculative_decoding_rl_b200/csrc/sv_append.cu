@@ -275,7 +275,7 @@ SV_DEV void append_page(const AppendParams &p, int b, int index, int job, bool h
     float *scale = p.scales + ((size_t)pr.blk * p.Hkv + hk) * 2 + (is_v ? 1 : 0);
     const int kept = min(PAGE, s.C - page * PAGE);
     const float old_scale = has_job && first < 0 ? *scale : 0.f;  // of rows that are there already
-    float y[NS][16], top = 0.f;
+    float y[NS][16], top = 0.f, not_finite = 0.f;
 #pragma unroll
     for (int st = 0; st < NS; ++st) {
         const int r = r0 + st * ROWS, i = first + r;
@@ -297,7 +297,19 @@ SV_DEV void append_page(const AppendParams &p, int b, int index, int job, bool h
                 else turn_slot<false>(tn, y[st]);
             }
         }
-        if (r < kept)
+        // rows past the last one are zeros here; x * 0 is NaN where x is not finite
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            top = fmaxf(top, fabsf(y[st][j]));
+            not_finite = fmaf(y[st][j], 0.f, not_finite);
+        }
+    }
+    // entries that are not finite are rare: without any, nothing below looks for them
+    const bool finite = __all_sync(0xffffffffu, not_finite == 0.f);
+    if (!finite) {
+        top = 0.f;
+#pragma unroll
+        for (int st = 0; st < NS; ++st)
 #pragma unroll
             for (int j = 0; j < 16; ++j) top = fmaxf(top, page8_mag(y[st][j]));
     }
@@ -307,6 +319,7 @@ SV_DEV void append_page(const AppendParams &p, int b, int index, int job, bool h
     if (!has_job) return;
     const int e = page8_exponent(fmaxf(tops[warp], tops[warp ^ 1]));
     const float inv = exp2_int(-e);
+    const uint64_t inv2 = (uint64_t)__float_as_uint(inv) << 32 | __float_as_uint(inv);
     if (lane == 0 && !(warp & 1)) *scale = exp2_int(e);
 #pragma unroll
     for (int st = 0; st < NS; ++st) {
@@ -314,7 +327,10 @@ SV_DEV void append_page(const AppendParams &p, int b, int index, int job, bool h
         if (r >= kept) continue;
         uint32_t w[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = page8_pair(y[st][2 * j], y[st][2 * j + 1], inv);
+        for (int j = 0; j < 8; ++j) {
+            const float2 x = mul2(y[st][2 * j], y[st][2 * j + 1], inv2);
+            w[j] = finite ? float2_to_e4m3x2(x.x, x.y) : page8_pair(y[st][2 * j], y[st][2 * j + 1], inv);
+        }
         reinterpret_cast<uint2 *>(dst + r * D)[slot.c1] = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
         reinterpret_cast<uint2 *>(dst + r * D)[slot.c2] = make_uint2(w[4] | w[5] << 16, w[6] | w[7] << 16);
     }
