@@ -16,7 +16,7 @@
 // sines) when there are few, so the rows themselves are asked for first.
 // Measured: 256 x 9 rows of 40 + 16 heads of 128 (67 MB) 13.3 us with L2 warm,
 // 18.8 us cold (0.54 of the copy rate); 16 ragged prompts of up to 1500 rows into
-// the 8-bit cache (259 MB) 75.8 us (0.52); 5 rows of one sequence 3.1 us.
+// the 8-bit cache (259 MB) 67 us (0.59); 5 rows of one sequence 3.1 us.
 #include "sv_page8.cuh"
 #include "sv_q8.h"
 
@@ -236,10 +236,16 @@ int rows_per_cta(const AppendParams &p, bool kv) {
     return rows;
 }
 
-__global__ void __launch_bounds__(AP_THREADS, 4) append_kernel(const __grid_constant__ AppendParams p, int rows) {
+// LOOP: `per` groups of rows to a CTA in place of one (the loop's registers cost the
+// rows of a verify step 8 %).
+template <bool LOOP>
+__global__ void __launch_bounds__(AP_THREADS, 4) append_kernel(const __grid_constant__ AppendParams p, int rows, int per) {
     const int b = blockIdx.y, group = AP_THREADS / rows, sub = threadIdx.x / group;
     if (p.status && blockIdx.x == 0) write_status(p, read_seq(p, b), b);
-    rotate_row<true>(p, b, blockIdx.x * rows + sub, threadIdx.x - sub * group, group);
+    if (!LOOP) return rotate_row<true>(p, b, blockIdx.x * rows + sub, threadIdx.x - sub * group, group);
+#pragma unroll 1
+    for (int g = 0; g < per; ++g)
+        rotate_row<true>(p, b, (blockIdx.x * per + g) * rows + sub, threadIdx.x - sub * group, group);
 }
 
 // One page of one KV head, K or V, by two warps, each half of its rows; the
@@ -336,21 +342,26 @@ SV_DEV void append_page(const AppendParams &p, int b, int index, int job, bool h
     }
 }
 
-// Grid: (pages a sequence's rows can touch x kv_parts, then its rows; sequences).
+// Grid: (pages a sequence's rows can touch x kv_parts, then its rows; sequences),
+// `per` pages or groups of rows to a CTA.
 template <int D>
-__global__ void __launch_bounds__(AP_THREADS, 3) append_q8_kernel(const __grid_constant__ AppendParams p, int pages,
-                                                                  int kv_parts, int rows) {
-    __shared__ float tops[AP_WARPS];
+__global__ void __launch_bounds__(AP_THREADS, 3) append_q8_kernel(const __grid_constant__ AppendParams p, int kv_ctas,
+                                                                  int kv_parts, int rows, int per) {
+    __shared__ float tops[2][AP_WARPS];
     const int b = blockIdx.y, warp = threadIdx.x >> 5;
     if (p.status && blockIdx.x == 0) write_status(p, read_seq(p, b), b);
-    const int x = blockIdx.x - pages * kv_parts;
+    const int x = blockIdx.x - kv_ctas;
     if (x < 0) {
         const int index = blockIdx.x / kv_parts, part = blockIdx.x - index * kv_parts;
         const int job = part * (AP_WARPS / 2) + (warp >> 1);
-        append_page<D>(p, b, index, job, job < 2 * p.Hkv, warp, threadIdx.x & 31, tops);
+#pragma unroll 1
+        for (int g = 0; g < per; ++g)
+            append_page<D>(p, b, index * per + g, job, job < 2 * p.Hkv, warp, threadIdx.x & 31, tops[g & 1]);
     } else {
         const int group = AP_THREADS / rows, sub = threadIdx.x / group;
-        rotate_row<false>(p, b, x * rows + sub, threadIdx.x - sub * group, group);
+#pragma unroll 1
+        for (int g = 0; g < per; ++g)
+            rotate_row<false>(p, b, (x * per + g) * rows + sub, threadIdx.x - sub * group, group);
     }
 }
 
@@ -360,19 +371,29 @@ cudaError_t launch_append(const AppendParams &params, bool q8, cudaStream_t stre
     AppendParams p = params;
     p.slots = p.R / 16 + ((p.D - p.R) / 8 + 1) / 2;
     const int rows = rows_per_cta(p, !q8);
-    const unsigned row_ctas = (unsigned)((p.N + rows - 1) / rows);
+    const long long groups = (p.N + rows - 1) / rows, pages = (p.N + PAGE - 2) / PAGE + 1;  // that N positions can touch
+    // Ragged prompts leave CTAs without rows, which still wait for their length:
+    // with many rows to a sequence a CTA goes on to the next ones (16 prompts of up
+    // to 1500 rows into the 8-bit cache: 75 us with one group to a CTA, 67 with four,
+    // 68 with eight).
+    const int per = p.new_lens && p.N >= 256 ? 4 : 1;
+    const long long row_ctas = (groups + per - 1) / per;
     if (!q8) {
-        append_kernel<<<dim3(row_ctas, (unsigned)p.B), AP_THREADS, 0, stream>>>(p, rows);
+        const dim3 grid((unsigned)row_ctas, (unsigned)p.B);
+        if (per > 1)
+            append_kernel<true><<<grid, AP_THREADS, 0, stream>>>(p, rows, per);
+        else
+            append_kernel<false><<<grid, AP_THREADS, 0, stream>>>(p, rows, per);
         return cudaGetLastError();
     }
-    const int pages = (p.N + PAGE - 2) / PAGE + 1;  // that N consecutive positions can touch
     const int kv_parts = (2 * p.Hkv + AP_WARPS / 2 - 1) / (AP_WARPS / 2);
-    if ((long long)pages * kv_parts + row_ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    const dim3 grid((unsigned)pages * kv_parts + (p.q ? row_ctas : 0u), (unsigned)p.B);
+    const long long kv_ctas = (pages + per - 1) / per * kv_parts;
+    if (kv_ctas + row_ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    const dim3 grid((unsigned)(kv_ctas + (p.q ? row_ctas : 0)), (unsigned)p.B);
     if (p.D == 128)
-        append_q8_kernel<128><<<grid, AP_THREADS, 0, stream>>>(p, pages, kv_parts, rows);
+        append_q8_kernel<128><<<grid, AP_THREADS, 0, stream>>>(p, (int)kv_ctas, kv_parts, rows, per);
     else
-        append_q8_kernel<64><<<grid, AP_THREADS, 0, stream>>>(p, pages, kv_parts, rows);
+        append_q8_kernel<64><<<grid, AP_THREADS, 0, stream>>>(p, (int)kv_ctas, kv_parts, rows, per);
     return cudaGetLastError();
 }
 

@@ -40,9 +40,9 @@
 //                zeroed before a tile goes to its product; the pages' scales.
 //
 // Measured at D = 128: 64 sequences of 512 to 32768 tokens, 45 rows a unit (1.05
-// GB) 256 us in short runs (4.1 TB/s; the loads alone would take 160 us), of which
+// GB) 262 us in short runs (4.0 TB/s; the loads alone would take 160 us), of which
 // a range's tile takes 1.9 us and a unit's start and end 7 us; 16 trees of 88 rows
-// over 24576 tokens (0.41 GB) 181 us. What bounds it is the softmax's instruction
+// over 24576 tokens (0.41 GB) 184 us. What bounds it is the softmax's instruction
 // stream, 3550 warp instructions a tile, not memory (50 %) or the tensor unit (43 %).
 #include <string.h>
 

@@ -111,6 +111,14 @@ def test_append_ragged_prompts_and_positions(q8):
 
 
 @pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("N,Hq,Hkv,D", [(256, 2, 1, 64), (300, 16, 2, 128), (259, 33, 3, 128)])
+def test_append_long_ragged_prompts(q8, N, Hq, Hkv, D):
+    # several groups of rows, or pages, to a CTA
+    nl = torch.tensor([N, 0, N - 255, 17, N - 1], dtype=torch.int32)
+    run_append(q8, 5, N, Hq, Hkv, D, D // 2, False, [N + 5, 30, N, 50, N - 1], seed=N, new_lens=nl, fused=True)
+
+
+@pytest.mark.parametrize("q8", [False, True])
 def test_append_flags_and_skips(q8):
     def spoil(qkv, pools, table, ctx, positions, nb):
         ctx[0] = 3                       # shorter than its new rows
