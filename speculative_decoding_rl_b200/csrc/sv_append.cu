@@ -249,14 +249,15 @@ __global__ void __launch_bounds__(AP_THREADS, 4) append_kernel(const __grid_cons
 }
 
 // One page of one KV head, K or V, by two warps, each half of its rows; the
-// whole CTA comes here for one page. tops: a float per warp.
+// whole CTA comes here for one page. tops: a float per warp. True where the CTA
+// passed the barrier, false (for every thread alike) where the page is skipped.
 template <int D>
-SV_DEV void append_page(const AppendParams &p, int b, int index, int job, bool has_job, int warp, int lane, float *tops) {
+SV_DEV bool append_page(const AppendParams &p, int b, int index, int job, bool has_job, int warp, int lane, float *tops) {
     // a lane holds one slot (two chunks) of NS of the page's rows
     constexpr int SLOTS = D / 16, ROWS = 32 / SLOTS, NS = PAGE / 2 / ROWS;
     const Seq s = read_seq(p, b);
     const int page = s.start / PAGE + index;
-    if (!s.ok || s.n == 0 || page * PAGE >= s.C) return;
+    if (!s.ok || s.n == 0 || page * PAGE >= s.C) return false;
     const int hk = job >> 1;
     const bool is_v = job & 1;
     const uint16_t *src = (is_v ? p.v : p.k) + (size_t)b * p.N * p.kv_stride + (size_t)hk * D;
@@ -276,7 +277,7 @@ SV_DEV void append_page(const AppendParams &p, int b, int index, int job, bool h
         }
     }
     const PageRows pr(p, s, b, page);
-    if (!pr.ok(p)) return;  // the same for every warp of the CTA
+    if (!pr.ok(p)) return false;  // the same for every warp of the CTA
     uint8_t *dst = static_cast<uint8_t *>(is_v ? p.v_pool : p.k_pool) + ((size_t)pr.blk * p.Hkv + hk) * PAGE * D;
     float *scale = p.scales + ((size_t)pr.blk * p.Hkv + hk) * 2 + (is_v ? 1 : 0);
     const int kept = min(PAGE, s.C - page * PAGE);
@@ -322,7 +323,7 @@ SV_DEV void append_page(const AppendParams &p, int b, int index, int job, bool h
     top = warp_max(has_job ? top : 0.f);
     if (lane == 0) tops[warp] = top;
     __syncthreads();  // both halves have read the page and its scale before one writes
-    if (!has_job) return;
+    if (!has_job) return true;
     const int e = page8_exponent(fmaxf(tops[warp], tops[warp ^ 1]));
     const float inv = exp2_int(-e);
     const uint64_t inv2 = (uint64_t)__float_as_uint(inv) << 32 | __float_as_uint(inv);
@@ -340,6 +341,7 @@ SV_DEV void append_page(const AppendParams &p, int b, int index, int job, bool h
         reinterpret_cast<uint2 *>(dst + r * D)[slot.c1] = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
         reinterpret_cast<uint2 *>(dst + r * D)[slot.c2] = make_uint2(w[4] | w[5] << 16, w[6] | w[7] << 16);
     }
+    return true;
 }
 
 // Grid: (pages a sequence's rows can touch x kv_parts, then its rows; sequences),
@@ -354,9 +356,13 @@ __global__ void __launch_bounds__(AP_THREADS, 3) append_q8_kernel(const __grid_c
     if (x < 0) {
         const int index = blockIdx.x / kv_parts, part = blockIdx.x - index * kv_parts;
         const int job = part * (AP_WARPS / 2) + (warp >> 1);
+        // the maxima of two pages in turn: a warp may write the next page's while its
+        // partner still reads this one's, and only the barrier of a page that is not
+        // skipped keeps it from the one after that
+        int turn = 0;
 #pragma unroll 1
         for (int g = 0; g < per; ++g)
-            append_page<D>(p, b, index * per + g, job, job < 2 * p.Hkv, warp, threadIdx.x & 31, tops[g & 1]);
+            turn ^= append_page<D>(p, b, index * per + g, job, job < 2 * p.Hkv, warp, threadIdx.x & 31, tops[turn]);
     } else {
         const int group = AP_THREADS / rows, sub = threadIdx.x / group;
 #pragma unroll 1
