@@ -97,6 +97,13 @@ constexpr int MAX_RING = 16;   // K and V slots of a range at most
 // raise waits until one passes P_MAX = 2^15, below fp16's and e5m2's largest
 // values; half of e5m2's smallest step is 2^-24 of the maximum.
 constexpr float P_SCALE = 128.f, P_UNSCALE = 1.f / 128.f, P_MAX = 32768.f;
+// A maximum is of score + log2(V's scale). From here on a score's spacing (2^-3)
+// would round that sum, and past 2^28 lose the scale or overshoot by more than the
+// weights have room for: the maximum is then kept in two parts, hi + lo, hi the
+// largest score alone and lo the largest (score - hi) + log2(V's scale), neither
+// of which rounds. Such a unit is rare: its tiles' scores are rewritten as
+// score - hi, so that the pass that makes the weights is the same.
+constexpr float TWO_PARTS_FROM = 1048576.f;
 // A range is at least this long: on small calls, shorter ranges would cost the
 // combine more partials than they save (one sequence of 6151 tokens: 17.4 us at 2,
 // 16.7 at 4, 18.5 at 6).
@@ -104,7 +111,7 @@ constexpr int MIN_WIDTH = 4;
 
 struct Q8Layout {
     uint32_t tile_bytes, off_k, off_q, q_bytes, off_p, p_bytes, off_bar, off_tp, off_cl, off_red, off_nm, off_as,
-        off_rowi, off_rowoff, off_umask, off_fin, off_qs, off_sc, off_vnan, off_misc, total;
+        off_rowi, off_rowoff, off_umask, off_nh, off_qs, off_sc, off_vnan, off_misc, total;
 };
 
 template <int D, int RP>
@@ -123,12 +130,13 @@ __host__ __device__ inline Q8Layout q8_layout(int NK, int NV, int B) {
     L.off_cl = L.off_tp + 4u * (B + 1);
     L.off_red = (L.off_cl + 4u * B + 15u) & ~15u;
     L.off_nm = L.off_red + 4u * 4 * S::NT * RP;    // [range][warp][RP] tile column maxima, or row sums
-    L.off_as = L.off_nm + 4u * S::NT * RP;         // [range][RP] running maxima, negated
+    L.off_as = L.off_nm + 4u * S::NT * RP;         // [range][RP] running maxima (or second parts), negated
     L.off_rowi = L.off_as + 4u * S::NT * RP;       // [range][RP] rescale factors
     L.off_rowoff = (L.off_rowi + 4u * RP + 15u) & ~15u;
     L.off_umask = L.off_rowoff + 4u * RP;
-    L.off_fin = L.off_umask + 8u * S::WGS * 64;    // [wg][64] mask words of the unit
-    L.off_qs = (L.off_fin + 4u * S::NT * RP + 15u) & ~15u;  // [range][RP] row sums of a finished unit
+    L.off_nh = L.off_umask + 8u * S::WGS * 64;     // [wg][64] mask words of the unit
+    // [range][RP] first parts of maxima in two parts, negated; factors of a finished unit
+    L.off_qs = (L.off_nh + 4u * S::NT * RP + 15u) & ~15u;
     L.off_sc = L.off_qs + 4u * S::NT * QS_RING * RP;        // [range][QS_RING][RP] query row scales
     L.off_vnan = L.off_sc + 8u * S::NT * SC_RING * SC_BATCH * PAGES_TILE;  // [range][batch][32] page scales (K, V)
     L.off_misc = L.off_vnan + 4u * S::NT * UNIT_RING;
@@ -651,11 +659,11 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
         float *red = reinterpret_cast<float *>(base + L.off_red) + r * 4 * RP + col0;  // [warp] * RP
         float *nm = reinterpret_cast<float *>(base + L.off_nm) + r * RP + col0;
         float *as = reinterpret_cast<float *>(base + L.off_as) + r * RP + col0;
-        float *lfin = reinterpret_cast<float *>(base + L.off_fin) + r * RP + col0;
+        float *nh = reinterpret_cast<float *>(base + L.off_nh) + r * RP + col0;
         uint64_t *umask = reinterpret_cast<uint64_t *>(base + L.off_umask) + wg * 64;
         float *qs_ring = reinterpret_cast<float *>(base + L.off_qs) + r * QS_RING * RP;
         const size_t slot_floats = slot_stride(p.rows_unit, D);
-        bool ok = true;
+        bool ok = true, split = false;  // split: the unit's maxima are in two parts
         int lu = -1, ub = 0, uhr = 0, uC = 0;
 
         auto warp_arrive = [&](uint64_t *b) {
@@ -724,12 +732,15 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
             float *slot = p.ws_partial + (size_t)(ub * ups + uhr + seg) * slot_floats;
             if (ell < CW) {
                 const float l = (red[ell] + red[RP + ell]) + (red[2 * RP + ell] + red[3 * RP + ell]);
-                // what O is multiplied by: a row that saw nothing gives 0
-                lfin[ell] = to_slot ? 1.f : l > 0.f || l != l ? 1.f / l : 0.f;
+                // in a slot the maximum is hi alone: lo, at most 100 either way, goes into the
+                // sums, which stay below 2^100 a key and 2^109 times the keys
+                const float back = split ? ex2_approx(-nm[ell]) : 1.f;
                 if (to_slot && ell < frows) {
-                    slot[(size_t)p.rows_unit * D + col0 + ell] = -nm[ell];
-                    slot[(size_t)p.rows_unit * D + p.rows_unit + col0 + ell] = l;
+                    slot[(size_t)p.rows_unit * D + col0 + ell] = split ? -nh[ell] : -nm[ell];
+                    slot[(size_t)p.rows_unit * D + p.rows_unit + col0 + ell] = l * back;
                 }
+                // what O is multiplied by, in nh's place: a row that saw nothing gives 0
+                nh[ell] = to_slot ? back : l > 0.f || l != l ? 1.f / l : 0.f;
             }
             wg_sync(1 + wg);
             if (!wait_w(&o_full[tlast % PB], (tlast / PB) & 1)) return false;
@@ -752,7 +763,7 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
                 tmem_wait_ld();
 #pragma unroll
                 for (int c4 = 0; c4 < CH / 4; ++c4) {
-                    const float4 f = reinterpret_cast<const float4 *>(lfin + c0)[c4];
+                    const float4 f = reinterpret_cast<const float4 *>(nh + c0)[c4];
                     o[c4 * 4] = o[c4 * 4] * P_UNSCALE * f.x;
                     o[c4 * 4 + 1] = o[c4 * 4 + 1] * P_UNSCALE * f.y;
                     o[c4 * 4 + 2] = o[c4 * 4 + 2] * P_UNSCALE * f.z;
@@ -831,7 +842,7 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
             const float2 scl = scr[sslot * 32 + lt % SC_BATCH * PAGES_TILE + ell / PAGE];
             if (lt % SC_BATCH == SC_BATCH - 1) warp_arrive(&sc_empty[sslot]);
             const float lv = __log2f(scl.y), ks1 = scl.x * p.scale_log2;
-            const uint64_t ksc = pack2(ks1, ks1);
+            uint64_t ksc = pack2(ks1, ks1);
             const uint64_t vsc = pack2(scl.y * P_SCALE, scl.y * P_SCALE);
             const float *qs = qs_ring + lu % QS_RING * RP + col0;
             const int sb = lt % SB;
@@ -873,12 +884,13 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
             uint8_t *pdst = p_buf + pb * L.p_bytes + ell * 16;
             auto p_at = [&](int c0) { return (col0 + c0) / 16 * GROUP + (col0 + c0) % 16; };
             if (lt >= PB && ok) ok = wait_w(&o_full[pb], ((lt - PB) / PB) & 1);  // P is free
-            const bool fresh = first;
-            bool raise = first, leave = false;
+            const bool fresh = first;  // a unit in two parts raises at every tile, before its weights are made
+            bool raise = first || split, leave = false;
             // a second raise in a row cannot come: the maxima are the tile's own then
 #pragma unroll 1
             for (int tries = 0;; ++tries) {
-                if (!raise) {
+                const bool counted = !raise;  // this tile's weights are in the row sums
+                if (counted) {
                     __half2 top2 = __float2half2_rn(0.f);
                     if (ok) {
 #pragma unroll 1
@@ -945,6 +957,7 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
                 }
                 if ((leave = wg_any(1 + wg, !ok))) break;
                 // tile column maxima over the 128 keys; this tile's weights out of the row sums
+                bool big = false;
 #pragma unroll 1
                 for (int c0 = 0; c0 < CW; c0 += CH) {
                     float y[CH], l[CH];
@@ -953,23 +966,57 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
                     tmem_wait_ld();
 #pragma unroll
                     for (int c = 0; c < CH; ++c) {
-                        const float e = y[c] * ks1, q = qs[c0 + c];
+                        const float e = __fmul_rn(y[c] * ks1, qs[c0 + c]);
                         // a sum that overflowed held nothing that counts beside the weight that made it so
-                        l[c] = fresh || l[c] == INFINITY ? 0.f : l[c] - ex2_approx(__fadd_rn(__fmul_rn(e, q), nm[c0 + c]));
-                        y[c] = __fadd_ru(__fmul_rn(e, q), lv);  // no weight passes 1, however large the scores
+                        l[c] = fresh || l[c] == INFINITY ? 0.f
+                               : counted                 ? l[c] - ex2_approx(__fadd_rn(e, nm[c0 + c]))
+                                                         : l[c];
+                        y[c] = __fadd_rn(e, lv);
                     }
                     tmem_store<CH>(tm_l + c0, l);
                     const float m = warp_reduce<CH, true>(y, lane);
+                    big |= fabsf(m) >= TWO_PARTS_FROM && fabsf(m) < INFINITY;
                     if (lane % (32 / CH) == 0) red[wiw * RP + c0 + lane / (32 / CH)] = m;
                 }
                 tmem_wait_st();
-                wg_sync(1 + wg);
+                auto tile_max = [&]() {  // of column ell
+                    return fmaxf(fmaxf(red[ell], red[RP + ell]), fmaxf(red[2 * RP + ell], red[3 * RP + ell]));
+                };
+                // once a unit's maxima have two parts, all its tiles' have
+                const bool were = split && !fresh;
+                split = wg_any(1 + wg, big || were);
+                float hi = 0.f, lo = 0.f;
+                if (ell < CW && !split) hi = tile_max();
+                if (__builtin_expect(split, 0)) {  // hi: the largest score; lo: what the scales add to it
+#pragma unroll 1
+                    for (int part = 0; part < 2; ++part) {
+#pragma unroll 1
+                        for (int c0 = 0; c0 < CW; c0 += CH) {
+                            float y[CH];
+                            tmem_load<CH>(saddr + c0, y);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < CH; ++c) {
+                                const float e = __fmul_rn(y[c] * ks1, qs[c0 + c]);
+                                y[c] = part ? __fadd_rn(__fsub_rn(e, as[c0 + c]), lv) : e;
+                            }
+                            const float m = warp_reduce<CH, true>(y, lane);
+                            if (lane % (32 / CH) == 0) red[wiw * RP + c0 + lane / (32 / CH)] = m;
+                        }
+                        wg_sync(1 + wg);
+                        if (ell < CW) (part ? lo : hi) = tile_max();
+                        if (part) break;
+                        if (ell < CW) as[ell] = hi;
+                        wg_sync(1 + wg);
+                    }
+                }
                 if (ell < CW) {
-                    const float m_old = fresh ? M_NONE : -nm[ell];
-                    const float rmax = fmaxf(fmaxf(red[ell], red[RP + ell]), fmaxf(red[2 * RP + ell], red[3 * RP + ell]));
-                    const float mx = fmaxf(m_old, rmax);  // stays M_NONE while nothing is visible
-                    nm[ell] = -mx;
-                    as[ell] = ex2_approx(m_old - mx);  // M_NONE - finite underflows to 0
+                    // h1 stays M_NONE while nothing is visible; M_NONE - finite underflows to 0
+                    const float h0 = fresh ? M_NONE : were ? -nh[ell] : -nm[ell], l0 = were ? -nm[ell] : 0.f;
+                    const float h1 = fmaxf(h0, hi), l1 = fmaxf((h0 - h1) + l0, (hi - h1) + lo);
+                    nm[ell] = split ? -l1 : -h1;
+                    nh[ell] = -h1;
+                    as[ell] = ex2_approx((h0 - h1) + (split ? l0 - l1 : 0.f));
                 }
                 wg_sync(1 + wg);
                 if (!fresh) {
@@ -990,6 +1037,24 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
                         }
                         tmem_wait_st();
                     }
+                }
+                if (__builtin_expect(split, 0)) {
+                    // in the scores' place what gives score - hi, exact where it counts, when
+                    // multiplied by the row's scale, a power of two (a NaN stays one)
+#pragma unroll 1
+                    for (int c0 = 0; c0 < CW; c0 += CH) {
+                        float y[CH];
+                        tmem_load<CH>(saddr + c0, y);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) {
+                            const float e = __fmul_rn(y[c] * ks1, qs[c0 + c]);
+                            y[c] = __fadd_rn(e, nh[c0 + c]) * __int_as_float(0x7F000000 - __float_as_int(qs[c0 + c]));
+                        }
+                        tmem_store<CH>(saddr + c0, y);
+                    }
+                    tmem_wait_st();
+                    ksc = pack2(1.f, 1.f);
                 }
                 raise = false;
             }

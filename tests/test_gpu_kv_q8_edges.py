@@ -3,7 +3,7 @@ bit, the attention within bounds that follow from its documented roundings."""
 import pytest
 import torch
 
-from test_gpu_kv_q8 import gen, run_append
+from test_gpu_kv_q8 import F8, gen, run_append, run_attend
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +31,63 @@ def test_append_of_long_ragged_prompts_skips_pages_among_others(how, D, Hkv):
                         positions[b, max(p * 16, start) - start + (p % 5 if p * 16 >= start else 0)] = -1 if p & 1 else 500
     run_append(True, len(lens), N, 4 if D == 128 else 5, Hkv, D, D, False, lens, seed=51, positions=pos,
                new_lens=nl, spoil=spoil, rows=500, fused=True)
+
+
+# ------------------------------------------------------------------ attention
+def one_dim_scores(size, tops):
+    """Scores along one dimension, whole numbers from -20 to 20 times `size`; the keys of `tops` (sequence, position)
+    stand above them at 22 * size."""
+    def spoil(q, kv, table, ctx, nb):
+        q.zero_()
+        q[..., 0] = size
+        kv[2][..., 0] = 1.0
+        kv[0].copy_(torch.zeros(kv[0].shape).to(F8))
+        kv[0][..., 0] = torch.randint(-20, 20, kv[0].shape[:3], generator=gen(3)).float().to(F8)
+        for b, t in tops:
+            kv[0][table[b, t // 16], :, t % 16, 0] = 22.0
+    return spoil
+
+
+def value(call, b, t):
+    """V of a key in 64 bits, [Hkv][D], and its scales."""
+    blk = int(call.block_table[b, t // 16])
+    sc = call.pools[2][blk, :, 1, None].cpu().double()
+    return call.pools[1][blk, :, t % 16].cpu().double() * sc, sc
+
+
+@pytest.mark.parametrize("size", [2.0 ** 17, 2.0 ** 23, 2.0 ** 28, 2.0 ** 30, 2.0 ** 60, 2.0 ** 120])
+@pytest.mark.parametrize("lo,hi", [(1, 5), (-40, -24), (90, 101), (-100, -90)])
+@pytest.mark.parametrize("N,Hq,D,lens", [(1, 4, 64, [1500, 20]), (5, 8, 128, [1500, 20]), (12, 8, 128, [60, 700]),
+                                         (16, 8, 64, [400, 20]), (11, 16, 128, [300, 24000])])
+def test_attention_huge_scores_whatever_the_scale_of_v(size, lo, hi, N, Hq, D, lens):
+    # scores whose spacing is far beyond log2 of V's scale; all weight on one key
+    tops = [(0, 41), (1, {20: 3, 700: 600, 24000: 17001}[lens[1]])]
+    call, got, want, tol = run_attend(N, Hq, 2, D, lens, seed=52, spoil=one_dim_scores(size, tops), lo=lo, hi=hi)
+    assert not call.status.any()
+    # the next key is exp(-2 * 2^17 / sqrt(D)) < 2^-300 lower. What is left of the bound: the weight enters the
+    # product rounded to 2^-9 of itself, the sum it is divided by is that weight in fp32 (2^-20 with the exponential),
+    # the output is rounded to bf16
+    for b, t in tops:
+        v = value(call, b, t)[0].repeat_interleave(Hq // 2, 0)[None].expand(N, Hq, D)
+        assert ((got[b] - v).abs() <= (2.0 ** -8 + 2.0 ** -9 + 2.0 ** -19) * v.abs()).all()
+
+
+@pytest.mark.parametrize("size", [2.0 ** 10, 2.0 ** 28, 2.0 ** 31, 2.0 ** 70])
+@pytest.mark.parametrize("gap", [0, 8, 14, 60, 90])
+def test_attention_equal_huge_scores_under_unlike_scales(size, gap):
+    # two keys with the same score in tiles of different ranges, V's scales 2^gap apart: the mean of their values
+    tops = [(0, 41), (0, 15000)]
+    more = one_dim_scores(size, tops)
+
+    def spoil(q, kv, table, ctx, nb):
+        more(q, kv, table, ctx, nb)
+        kv[2][table[0, 41 // 16], :, 1] = 2.0 ** (gap // 2)
+        kv[2][table[0, 15000 // 16], :, 1] = 2.0 ** (gap // 2 - gap)
+    call, got, want, tol = run_attend(5, 8, 2, 128, [20000], seed=53, spoil=spoil)
+    assert not call.status.any()
+    (v0, s0), (v1, s1) = (value(call, 0, t) for _, t in tops)
+    # each weight is off by 2^-9 of itself or, far below the largest weight times scale, by 2^-24 of that
+    bound = 2.0 ** -8 * (v0 + v1).abs() / 2 + (2.0 ** -9 + 2.0 ** -19) * (v0.abs() + v1.abs()) / 2 \
+        + 2.0 ** -24 * s0 / 2 * (v1 / s1).abs()
+    v, bound = (x.repeat_interleave(4, 0)[None].expand(5, 8, 128) for x in ((v0 + v1) / 2, bound))
+    assert ((got[0] - v).abs() <= bound).all()
