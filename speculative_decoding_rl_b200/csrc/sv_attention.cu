@@ -829,11 +829,17 @@ __global__ void __launch_bounds__(32 * COMBINE_ROWS, MIN_CTAS) attn_combine_kern
     float M = mk;
     for (int k = lane + 32; k < n; k += 32) M = fmaxf(M, __ldcg(seg0 + (size_t)k * sf + (size_t)RU * D + r));
     M = warp_max(M);
-    const float wl = lane < n ? exp2f(mk - M) : 0.f;  // an empty segment holds l = 0
-    float L = wl * lk;
+    // The 8-bit cache's maxima hold V's scale, which may be 2^200 apart, and the
+    // sums the inverse of it: the factor comes to them in two halves.
+    constexpr float HALF = UC == UNIT_COST_Q8 ? 0.5f : 1.f;
+    auto scaled = [](float w, float l) { return HALF == 1.f ? w * l : w * l * w; };
+    const float wh = lane < n ? exp2f((mk - M) * HALF) : 0.f;  // an empty segment holds l = 0
+    const float wl = HALF == 1.f ? wh : wh * wh;
+    float L = scaled(wh, lk);
     for (int k = lane + 32; k < n; k += 32) {
         const float *sg = seg0 + (size_t)k * sf + (size_t)RU * D;
-        L = fmaf(exp2f(__ldcg(sg + r) - M), __ldcg(sg + RU + r), L);
+        const float w = exp2f((__ldcg(sg + r) - M) * HALF), l = __ldcg(sg + RU + r);
+        L = HALF == 1.f ? fmaf(w, l, L) : L + scaled(w, l);
     }
     L = warp_sum(L);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);

@@ -131,7 +131,7 @@ __host__ __device__ inline Q8Layout q8_layout(int NK, int NV, int B) {
     L.off_red = (L.off_cl + 4u * B + 15u) & ~15u;
     L.off_nm = L.off_red + 4u * 4 * S::NT * RP;    // [range][warp][RP] tile column maxima, or row sums
     L.off_as = L.off_nm + 4u * S::NT * RP;         // [range][RP] running maxima (or second parts), negated
-    L.off_rowi = L.off_as + 4u * S::NT * RP;       // [range][RP] rescale factors
+    L.off_rowi = L.off_as + 4u * S::NT * RP;       // [range][RP] roots of the rescale factors
     L.off_rowoff = (L.off_rowi + 4u * RP + 15u) & ~15u;
     L.off_umask = L.off_rowoff + 4u * RP;
     L.off_nh = L.off_umask + 8u * S::WGS * 64;     // [wg][64] mask words of the unit
@@ -1016,7 +1016,8 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
                     const float h1 = fmaxf(h0, hi), l1 = fmaxf((h0 - h1) + l0, (hi - h1) + lo);
                     nm[ell] = split ? -l1 : -h1;
                     nh[ell] = -h1;
-                    as[ell] = ex2_approx((h0 - h1) + (split ? l0 - l1 : 0.f));
+                    // the factor's root: V's scales may be 2^200 apart, and a row sum as large
+                    as[ell] = ex2_approx(0.5f * ((h0 - h1) + (split ? l0 - l1 : 0.f)));
                 }
                 wg_sync(1 + wg);
                 if (!fresh) {
@@ -1032,7 +1033,7 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
                             tmem_load<CH>(at, o);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int c = 0; c < CH; ++c) o[c] *= as[c0 + c];
+                            for (int c = 0; c < CH; ++c) o[c] = o[c] * as[c0 + c] * as[c0 + c];
                             tmem_store<CH>(at, o);
                         }
                         tmem_wait_st();

@@ -91,3 +91,32 @@ def test_attention_equal_huge_scores_under_unlike_scales(size, gap):
         + 2.0 ** -24 * s0 / 2 * (v1 / s1).abs()
     v, bound = (x.repeat_interleave(4, 0)[None].expand(5, 8, 128) for x in ((v0 + v1) / 2, bound))
     assert ((got[0] - v).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("gap", [120, 130, 160, 200])
+@pytest.mark.parametrize("D,N,Hq,C", [(128, 5, 8, 300), (64, 1, 4, 700), (128, 11, 16, 400), (128, 5, 8, 20000)])
+@pytest.mark.parametrize("last", [True, False])
+def test_attention_scales_of_v_further_apart_than_fp32(gap, D, N, Hq, C, last):
+    # keys of equal weight whose V scales differ by 2^gap: those of the small scale count in the sum of the weights
+    # although their part of the output is nothing beside the others'
+    def spoil(q, kv, table, ctx, nb):
+        kv[0].copy_(torch.zeros(kv[0].shape).to(F8))
+        kv[2][..., 1] = 2.0 ** -(gap // 2)
+        for p in range(-(-C // 16)):
+            if (p >= C // 32) == last:
+                kv[2][table[0, p], :, 1] = 2.0 ** (gap - gap // 2)
+    call, got, want, tol = run_attend(N, Hq, 2, D, [C], seed=54, spoil=spoil)
+    assert not call.status.any()
+    # every weight is 1 / (keys seen), exact but for 2^-20; what is left of the bound: the weights' 2^-9, 2^-24 of the
+    # largest weight times scale for each of the others, and the output's rounding
+    sc = call.pools[2][call.block_table[0].long(), :, 1].cpu().double()                        # [pages][Hkv]
+    v = call.pools[1][call.block_table[0].long()].cpu().double() * sc[..., None, None]
+    v = v.transpose(0, 1).reshape(2, -1, D)[:, :C]                                             # [Hkv][C][D]
+    v8 = (v / sc.T.repeat_interleave(16, 1)[:, :C, None]).abs()
+    for i in range(N):
+        n = C - N + i + 1
+        o, A = v[:, :n].sum(1) / n, v[:, :n].abs().sum(1) / n
+        bound = 2.0 ** -8 * o.abs() + (2.0 ** -9 + 2.0 ** -19) * A + 2.0 ** -24 * sc.max() / n * v8[:, :n].sum(1)
+        for h in range(Hq):
+            kvh = h // (Hq // 2)
+            assert ((got[0, i, h] - o[kvh]).abs() <= bound[kvh]).all()
