@@ -20,6 +20,11 @@
  *                              SV_FLAG_TIMEOUT, and that the context is still
  *                              usable afterwards. Nothing faults or hangs: the
  *                              kernel takes its ordinary abort path.
+ *   sv_testing_verify_attention_q8_stalled
+ *                              the same for sv_verify_attention_q8, whose roles
+ *                              wait for one another in more ways: the caller
+ *                              says which role does nothing, so that the others'
+ *                              waits run out.
  * Conventions as in specverify.h: device pointers owned by the caller,
  * asynchronous on `stream`, argument errors returned before any launch.
  */
@@ -49,6 +54,18 @@ SV_API sv_status sv_testing_verify_attention_stalled(const sv_attn_desc *desc, c
                                                      void *out, void *workspace, size_t workspace_bytes,
                                                      int32_t *status_flags, uint64_t wait_limit_ns,
                                                      void *stream);
+
+/* The same over the 8-bit cache. role: which warps of each CTA's first work range
+ * do nothing (SV_ERR_INVALID_ARG for any other value): waits of the other roles run
+ * out, and the CTA's other work range learns of it. Expects a sequence with at least one
+ * key. */
+enum { SV_STALL_SOFTMAX = 1, SV_STALL_MMA = 2, SV_STALL_LOADS = 3, SV_STALL_AUX = 4 };
+
+SV_API sv_status sv_testing_verify_attention_q8_stalled(const sv_attn_desc *desc, const void *q, const sv_kv_q8 *kv,
+                                                        const int32_t *block_table, const int32_t *ctx_lens,
+                                                        const uint64_t *draft_mask, void *out, void *workspace,
+                                                        size_t workspace_bytes, int32_t *status_flags,
+                                                        uint64_t wait_limit_ns, int32_t role, void *stream);
 
 #ifdef __cplusplus
 }

@@ -24,7 +24,8 @@ __all__ = [
     "sv_verify_attention_q8", "sv_kv_commit_q8", "make_kv_q8_layers", "SdController", "SvCtlConfig", "SvHistoryDesc",
     "sv_history_draft",
     "sv_status_string", "sv_last_error", "sv_version", "library_path",
-    "sv_testing_philox4x32_10", "sv_testing_verify_attention_stalled", "SV_FLAG_TIMEOUT",
+    "sv_testing_philox4x32_10", "sv_testing_verify_attention_stalled", "sv_testing_verify_attention_q8_stalled",
+    "SV_STALL_SOFTMAX", "SV_STALL_MMA", "SV_STALL_LOADS", "SV_STALL_AUX", "SV_FLAG_TIMEOUT",
     "SV_FLAG_NONFINITE", "SV_FLAG_BAD_CONTEXT", "SV_FLAG_BAD_TOKEN", "SV_FLAG_BAD_BLOCK",
 ]
 
@@ -177,6 +178,9 @@ def _load() -> C.CDLL:
     L.sv_testing_verify_attention_stalled.argtypes = [C.POINTER(SvAttnDesc), P, C.POINTER(SvPagedKV), P, P, P, P,
                                                       P, sz, P, u64, P]
     L.sv_testing_verify_attention_stalled.restype = C.c_int
+    L.sv_testing_verify_attention_q8_stalled.argtypes = [C.POINTER(SvAttnDesc), P, C.POINTER(SvKVQ8), P, P, P, P, P,
+                                                         sz, P, u64, i32, P]
+    L.sv_testing_verify_attention_q8_stalled.restype = C.c_int
     L.sv_status_string.argtypes = [C.c_int]
     L.sv_status_string.restype = C.c_char_p
     L.sv_last_error.argtypes = []
@@ -484,6 +488,20 @@ def sv_testing_verify_attention_stalled(desc: SvAttnDesc, q, paged_kv: SvPagedKV
                                                     _ptr(ctx_lens), _ptr(draft_mask), _ptr(out), _ptr(workspace),
                                                     int(workspace_bytes), _ptr(status_flags), int(wait_limit_ns),
                                                     _stream(stream)))
+
+
+SV_STALL_SOFTMAX, SV_STALL_MMA, SV_STALL_LOADS, SV_STALL_AUX = 1, 2, 3, 4
+
+
+def sv_testing_verify_attention_q8_stalled(desc: SvAttnDesc, q, kv: SvKVQ8, block_table, ctx_lens, draft_mask, out,
+                                           workspace, workspace_bytes: int, status_flags, wait_limit_ns: int,
+                                           role: int, stream=None) -> None:
+    """Test hook: sv_verify_attention_q8 in which one role (SV_STALL_*) of every CTA does nothing and the
+    others' waits run out after wait_limit_ns; every sequence comes back flagged SV_FLAG_TIMEOUT."""
+    _check(_L().sv_testing_verify_attention_q8_stalled(C.byref(desc), _ptr(q), C.byref(kv), _ptr(block_table),
+                                                       _ptr(ctx_lens), _ptr(draft_mask), _ptr(out), _ptr(workspace),
+                                                       int(workspace_bytes), _ptr(status_flags), int(wait_limit_ns),
+                                                       int(role), _stream(stream)))
 
 
 def default_ctl_config() -> SvCtlConfig:

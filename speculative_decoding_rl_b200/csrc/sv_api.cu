@@ -394,6 +394,54 @@ sv_status check_commit_arrays(const sv_attn_desc *d, const int32_t *block_table,
 
 }  // namespace
 
+namespace sv {
+
+sv_status verify_attention_q8_entry(const sv_attn_desc *d, const void *q, const sv_kv_q8 *kv,
+                                    const int32_t *block_table, const int32_t *ctx_lens,
+                                    const uint64_t *draft_mask, void *out, void *workspace,
+                                    size_t workspace_bytes, int32_t *status_flags, void *stream,
+                                    uint64_t wait_limit_ns, int stall) {
+    sv_status s = check_attn_desc(d);
+    if (s != SV_OK) return s;
+    if (d->num_seqs == 0) return SV_OK;
+    if ((s = check_q8(kv)) != SV_OK) return s;
+    const sv_paged_kv pools = {kv->k_pool, kv->v_pool};
+    if ((s = check_attn_ptrs(q, &pools, block_table, ctx_lens, draft_mask, out, status_flags)) != SV_OK) return s;
+    {
+        // units are read and written in any order: no output over an input or another output
+        const size_t rows = (size_t)d->num_seqs * d->num_q_rows, B4 = (size_t)d->num_seqs * 4;
+        const size_t heads = (size_t)d->num_blocks * d->num_kv_heads, io = rows * d->num_q_heads * d->head_dim * 2;
+        const size_t pool = heads * sv::PAGE * d->head_dim;
+        const void *o[] = {out, workspace, status_flags};
+        const size_t ob[] = {io, workspace_bytes, B4};
+        const void *in[] = {q, kv->k_pool, kv->v_pool, kv->scales, block_table, ctx_lens, draft_mask};
+        const size_t ib[] = {io, pool, pool, heads * 8, B4 * (size_t)d->max_blocks_per_seq, B4, rows * 8};
+        for (int i = 0; i < 3; ++i) {
+            for (int j = 0; j < 7; ++j)
+                if (overlaps(o[i], ob[i], in[j], ib[j]))
+                    return fail(SV_ERR_INVALID_ARG, "out, workspace and status_flags must not overlap an input");
+            for (int j = 0; j < i; ++j)
+                if (overlaps(o[i], ob[i], o[j], ob[j]))
+                    return fail(SV_ERR_INVALID_ARG, "out, workspace and status_flags must not overlap");
+        }
+    }
+    const int ctas = sv::attention_num_ctas();
+    if (ctas <= 0) return fail(SV_ERR_CUDA, "cannot query the current device");
+    const size_t need = sv::attention_q8_workspace_bytes(d->num_seqs, d->num_q_rows, d->num_q_heads,
+                                                         d->num_kv_heads, d->head_dim, ctas);
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 256))
+        return fail(SV_ERR_WORKSPACE, "workspace must be 256-byte aligned and hold %zu bytes", need);
+    sv::AttnParams p =
+        attn_params(d, q, &pools, block_table, ctx_lens, draft_mask, out, workspace, status_flags, ctas);
+    p.wait_limit_ns = wait_limit_ns;
+    p.stall = stall;
+    cudaError_t e = sv::launch_attention_q8(p, kv->scales, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(SV_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
+    return SV_OK;
+}
+
+}  // namespace sv
+
 extern "C" {
 
 size_t sv_accept_workspace_size(const sv_accept_desc *d) {
@@ -510,41 +558,8 @@ sv_status sv_verify_attention_q8(const sv_attn_desc *d, const void *q, const sv_
                                  const int32_t *block_table, const int32_t *ctx_lens,
                                  const uint64_t *draft_mask, void *out, void *workspace,
                                  size_t workspace_bytes, int32_t *status_flags, void *stream) {
-    sv_status s = check_attn_desc(d);
-    if (s != SV_OK) return s;
-    if (d->num_seqs == 0) return SV_OK;
-    if ((s = check_q8(kv)) != SV_OK) return s;
-    const sv_paged_kv pools = {kv->k_pool, kv->v_pool};
-    if ((s = check_attn_ptrs(q, &pools, block_table, ctx_lens, draft_mask, out, status_flags)) != SV_OK) return s;
-    {
-        // units are read and written in any order: no output over an input or another output
-        const size_t rows = (size_t)d->num_seqs * d->num_q_rows, B4 = (size_t)d->num_seqs * 4;
-        const size_t heads = (size_t)d->num_blocks * d->num_kv_heads, io = rows * d->num_q_heads * d->head_dim * 2;
-        const size_t pool = heads * sv::PAGE * d->head_dim;
-        const void *o[] = {out, workspace, status_flags};
-        const size_t ob[] = {io, workspace_bytes, B4};
-        const void *in[] = {q, kv->k_pool, kv->v_pool, kv->scales, block_table, ctx_lens, draft_mask};
-        const size_t ib[] = {io, pool, pool, heads * 8, B4 * (size_t)d->max_blocks_per_seq, B4, rows * 8};
-        for (int i = 0; i < 3; ++i) {
-            for (int j = 0; j < 7; ++j)
-                if (overlaps(o[i], ob[i], in[j], ib[j]))
-                    return fail(SV_ERR_INVALID_ARG, "out, workspace and status_flags must not overlap an input");
-            for (int j = 0; j < i; ++j)
-                if (overlaps(o[i], ob[i], o[j], ob[j]))
-                    return fail(SV_ERR_INVALID_ARG, "out, workspace and status_flags must not overlap");
-        }
-    }
-    const int ctas = sv::attention_num_ctas();
-    if (ctas <= 0) return fail(SV_ERR_CUDA, "cannot query the current device");
-    const size_t need = sv::attention_q8_workspace_bytes(d->num_seqs, d->num_q_rows, d->num_q_heads,
-                                                         d->num_kv_heads, d->head_dim, ctas);
-    if (!workspace || workspace_bytes < need || !aligned(workspace, 256))
-        return fail(SV_ERR_WORKSPACE, "workspace must be 256-byte aligned and hold %zu bytes", need);
-    const sv::AttnParams p =
-        attn_params(d, q, &pools, block_table, ctx_lens, draft_mask, out, workspace, status_flags, ctas);
-    cudaError_t e = sv::launch_attention_q8(p, kv->scales, static_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return fail(SV_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
-    return SV_OK;
+    return sv::verify_attention_q8_entry(d, q, kv, block_table, ctx_lens, draft_mask, out, workspace, workspace_bytes,
+                                         status_flags, stream, 2000000000ull, 0);
 }
 
 sv_status sv_kv_commit_q8(const sv_attn_desc *d, int32_t num_layers, const sv_kv_q8 *layers,

@@ -48,6 +48,7 @@
 
 #include <type_traits>
 
+#include "../../include/specverify_testing.h"
 #include "sv_page8.cuh"
 #include "sv_q8.h"
 #include "sv_schedule.cuh"
@@ -150,6 +151,7 @@ struct Q8Params {
     AttnParams a;  // num_ctas counts ranges
     const float2 *scales;
     int NK, NV, Nc;
+    uint32_t wait_ns;  // bound of a wait
 };
 
 // A lane's D/16 entries of a query row, in bf16 bits, as two 8-bit words' worth of
@@ -276,14 +278,20 @@ SV_DEV uint64_t sub_max(uint64_t x, uint64_t nm) {
 }
 
 // Bounded wait on a phase, in few instructions (there are two dozen of them in
-// the kernel): gives up after WAIT_TRIES tries, which take a second or a few, or
-// once another thread has raised *abort; raises it then. (A suspend-time hint and
-// sleeps between the tries of the warps that feed the softmax measured the same.)
-constexpr uint32_t WAIT_TRIES = 1u << 23;
-SV_DEV bool wait_phase(uint64_t *b, uint32_t parity, volatile int *abort) {
-    bool done = mbar_try_wait(b, parity);
+// the kernel): gives up limit_ns after its first try, or once another thread has raised
+// *abort; raises it then. (A count of tries would be no bound: a try takes 80 ns to 4 us.)
+SV_DEV uint32_t clock_ns() {
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
+}
+SV_DEV bool wait_phase(uint64_t *b, uint32_t parity, volatile int *abort, uint32_t limit_ns) {
+    if (mbar_try_wait(b, parity)) return true;
+    const uint32_t t0 = clock_ns();
+    bool done;
 #pragma unroll 1
-    for (uint32_t i = 0; !done && i < WAIT_TRIES && !*abort; ++i) done = mbar_try_wait(b, parity);
+    do done = mbar_try_wait(b, parity);
+    while (!done && !*abort && clock_ns() - t0 <= limit_ns);
     if (!done) *abort = 1;
     return done;
 }
@@ -391,10 +399,14 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
     tc_fence_after();
     const uint32_t tmem = *tmem_slot + r * S::R_COLS;
     const TileInfo t_first{scratch[8 * r], scratch[8 * r + 1], scratch[8 * r + 2], scratch[8 * r + 3]};
-    const int ntiles = scratch[8 * r + 4];
+    // Test hook: to one role of the CTA's first range there are no tiles, so that the
+    // others wait for what never comes.
+    const int role = warp < WARP_LD ? SV_STALL_SOFTMAX
+                                    : warp < WARP_MMA ? SV_STALL_LOADS : warp < WARP_AUX ? SV_STALL_MMA : SV_STALL_AUX;
+    const int ntiles = p.stall == role && r == 0 ? 0 : scratch[8 * r + 4];
 
     auto wait_w = [&](uint64_t *b, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, wait_phase(b, parity, abort_flag));
+        return __all_sync(0xffffffffu, wait_phase(b, parity, abort_flag, P.wait_ns));
     };
 
     if (warp >= WARP_AUX) {
@@ -532,7 +544,7 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
             TileInfo tq = t_first, tp = tq;
             int lu = -1;
             auto wait1 = [&](uint64_t *b, uint32_t parity) {
-                return wait_phase(b, parity, abort_flag);
+                return wait_phase(b, parity, abort_flag, P.wait_ns);
             };
             auto issue_qk = [&](int t) -> bool {
                 if (t == 0 || tq.j == 0) {
@@ -636,7 +648,9 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
             idv = ids;
             hv = h;
         }
-        if (*abort_flag && lane == 0) {  // this range's own copies land before the CTA can exit
+        // Copies that nobody waited for, because someone gave up, land before the CTA can
+        // exit. Once the range's products are through, all were waited for.
+        if (lane == 0 && !(wait_phase(done_bar, 0, abort_flag, P.wait_ns) && !*abort_flag)) {
 #pragma unroll 1
             for (int i = max(0, issued[0] - NK); i < issued[0]; ++i)
                 mbar_wait_time(&k_full[i % NK], (i / NK) & 1, WAIT_LIMIT_NS);
@@ -1146,6 +1160,7 @@ cudaError_t launch_attention_q8(const AttnParams &p, const float *scales, cudaSt
     P.a = p;
     P.a.min_width = MIN_WIDTH;
     P.scales = reinterpret_cast<const float2 *>(scales);
+    P.wait_ns = (uint32_t)p.wait_limit_ns;
     int RU, RC;
     row_chunks(p.N, p.G, &RU, &RC, &P.Nc);
     if (!encode_pool_q8(&P.tm_k, p.k_pool, p.num_blocks, p.Hkv, p.D) ||

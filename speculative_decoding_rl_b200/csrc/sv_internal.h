@@ -78,7 +78,8 @@ struct AttnParams {
     // kernel runs; the shared-prefix kernel that follows merges each row.
     int all_slots;
     // Bound of every device-side wait (2 s). Test hooks shorten it, and with
-    // stall set make one wait per CTA run out (see sv_testing_*).
+    // stall set make one wait per CTA run out (see sv_testing_*); the 8-bit cache's
+    // kernel takes which of its roles does nothing (SV_STALL_*).
     uint64_t wait_limit_ns;
     int stall;
 };
@@ -149,7 +150,12 @@ cudaError_t launch_history_draft(const HistoryLaunch &h, cudaStream_t stream);
 // Sets the text sv_last_error() returns on the calling thread.
 void record_error(const char *msg);
 
-// sv_verify_attention with its wait bound and the stall test hook exposed.
+// sv_verify_attention and sv_verify_attention_q8 with their wait bound and the stall test hook exposed.
+sv_status verify_attention_q8_entry(const sv_attn_desc *d, const void *q, const sv_kv_q8 *kv,
+                                    const int32_t *block_table, const int32_t *ctx_lens,
+                                    const uint64_t *draft_mask, void *out, void *workspace,
+                                    size_t workspace_bytes, int32_t *status_flags, void *stream,
+                                    uint64_t wait_limit_ns, int stall);
 sv_status verify_attention_entry(const sv_attn_desc *d, const void *q, const sv_paged_kv *kv,
                                  const int32_t *block_table, const int32_t *ctx_lens,
                                  const uint64_t *draft_mask, void *out, void *workspace,

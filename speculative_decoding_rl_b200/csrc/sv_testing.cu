@@ -1,5 +1,5 @@
 // Test hooks of libspecverify (include/specverify_testing.h): the device Philox
-// block function over a list of counters, and the attention call with one wait
+// block function over a list of counters, and the attention calls with one wait
 // per CTA made to run out.
 #include "../../include/specverify_testing.h"
 #include "sv_device.cuh"
@@ -53,4 +53,21 @@ extern "C" sv_status sv_testing_verify_attention_stalled(const sv_attn_desc *des
     }
     return sv::verify_attention_entry(desc, q, paged_kv, block_table, ctx_lens, draft_mask, out, workspace,
                                       workspace_bytes, status_flags, stream, wait_limit_ns, 1);
+}
+
+extern "C" sv_status sv_testing_verify_attention_q8_stalled(const sv_attn_desc *desc, const void *q, const sv_kv_q8 *kv,
+                                                            const int32_t *block_table, const int32_t *ctx_lens,
+                                                            const uint64_t *draft_mask, void *out, void *workspace,
+                                                            size_t workspace_bytes, int32_t *status_flags,
+                                                            uint64_t wait_limit_ns, int32_t role, void *stream) {
+    if (wait_limit_ns < 1000000ull || wait_limit_ns > 2000000000ull) {
+        sv::record_error("wait_limit_ns must be in [1 ms, 2 s]");
+        return SV_ERR_INVALID_ARG;
+    }
+    if (role < SV_STALL_SOFTMAX || role > SV_STALL_AUX) {
+        sv::record_error("role must be one of SV_STALL_*");
+        return SV_ERR_INVALID_ARG;
+    }
+    return sv::verify_attention_q8_entry(desc, q, kv, block_table, ctx_lens, draft_mask, out, workspace,
+                                         workspace_bytes, status_flags, stream, wait_limit_ns, role);
 }

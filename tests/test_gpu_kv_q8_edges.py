@@ -1,8 +1,11 @@
 """The 8-bit KV cache's calls where they are easily wrong. What append and commit leave in memory is compared bit for
 bit, the attention within bounds that follow from its documented roundings."""
+import time
+
 import pytest
 import torch
 
+import speculative_decoding_rl_b200 as sv
 from test_gpu_kv_q8 import F8, gen, run_append, run_attend
 
 pytestmark = pytest.mark.gpu
@@ -120,3 +123,25 @@ def test_attention_scales_of_v_further_apart_than_fp32(gap, D, N, Hq, C, last):
         for h in range(Hq):
             kvh = h // (Hq // 2)
             assert ((got[0, i, h] - o[kvh]).abs() <= bound[kvh]).all()
+
+
+@pytest.mark.parametrize("role", [sv.SV_STALL_SOFTMAX, sv.SV_STALL_MMA, sv.SV_STALL_LOADS, sv.SV_STALL_AUX])
+@pytest.mark.parametrize("limit_ms", [5, 50])
+@pytest.mark.parametrize("N,Hq,D,lens", [(1, 4, 64, [30, 9000]), (5, 8, 128, [900, 2100, 37, 40000, 640]),
+                                         (9, 10, 128, [3000]), (16, 8, 64, [5000, 16]), (11, 16, 128, [11, 30000])])
+def test_attention_wait_that_runs_out(role, limit_ms, N, Hq, D, lens):
+    # one role of every CTA does nothing and the others' waits run out: the call returns within its limits, flags every
+    # sequence, and leaves nothing behind that the next call would notice
+    call, got, want, tol = run_attend(N, Hq, 2, D, lens, seed=55)
+    status = torch.full((len(lens),), -1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    sv.sv_testing_verify_attention_q8_stalled(call.desc, call.q, call.kv, call.block_table, call.ctx_lens, call.mask,
+                                              call.out, call.workspace, call.ws_bytes, status, limit_ms * 1_000_000,
+                                              role)
+    torch.cuda.synchronize()
+    elapsed = time.perf_counter() - t0
+    assert (status.cpu() & sv.SV_FLAG_TIMEOUT).all(), status
+    assert limit_ms / 1000 <= elapsed < 4.0, elapsed  # the limit, and 2 s at most for copies and products in flight
+    assert torch.equal(call.run().cpu().double(), got)
+    assert not call.status.any()
