@@ -356,7 +356,8 @@ SV_API sv_status sv_kv_append(const sv_attn_desc *desc, const sv_rope_desc *rope
  * drafts leave no trace: the scale only depends on the rows kept. Entries that
  * are not finite are stored as NaN. The attention takes any scales in
  * [2^-100, 2^100] (smaller ones, zero too, count as 2^-100), for instance from a
- * calibration; a page that a call then writes to is brought to its power of two.
+ * calibration; a page that a call then writes to is brought to its power of two,
+ * its entries standing for what the attention takes them for.
  */
 typedef struct {
     void *k_pool;                /* e4m3 [num_blocks][Hkv][16][D] */

@@ -281,7 +281,7 @@ SV_DEV bool append_page(const AppendParams &p, int b, int index, int job, bool h
     uint8_t *dst = static_cast<uint8_t *>(is_v ? p.v_pool : p.k_pool) + ((size_t)pr.blk * p.Hkv + hk) * PAGE * D;
     float *scale = p.scales + ((size_t)pr.blk * p.Hkv + hk) * 2 + (is_v ? 1 : 0);
     const int kept = min(PAGE, s.C - page * PAGE);
-    const float old_scale = has_job && first < 0 ? *scale : 0.f;  // of rows that are there already
+    const float old_scale = has_job && first < 0 ? page8_scale(*scale) : 0.f;  // of rows that are there already
     float y[NS][16], top = 0.f, not_finite = 0.f;
 #pragma unroll
     for (int st = 0; st < NS; ++st) {

@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
         auto batch_publish = [&](int batch) -> bool {
             const int slot = batch % SC_RING;
             if (!wait_w(&sc_empty[slot], (batch / SC_RING & 1) ^ 1)) return false;
-            scr[slot * 32 + lane] = make_float2(fmaxf(sc.x, PAGE8_SCALE_MIN), fmaxf(sc.y, PAGE8_SCALE_MIN));
+            scr[slot * 32 + lane] = make_float2(page8_scale(sc.x), page8_scale(sc.y));
             __syncwarp();
             if (lane == 0) mbar_arrive(&sc_full[slot]);
             return true;

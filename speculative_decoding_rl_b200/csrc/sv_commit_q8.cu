@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(32 * CQ_WARPS, 3) kv_commit_q8_kernel(const __
             for (int st = 0; st < Page8<D>::STEPS; ++st) {
                 const size_t at = (size_t)(from[st] / PAGE) * P.Hkv + h;
                 raw[st] = *reinterpret_cast<const uint2 *>(pool + (at * PAGE + from[st] % PAGE) * D + Page8<D>::col(lane));
-                scale[st] = layer.scales[2 * at + is_v];
+                scale[st] = page8_scale(layer.scales[2 * at + is_v]);
             }
             const size_t at = (size_t)dst * P.Hkv + h;
             __syncwarp();  // every lane has read the page before one writes it

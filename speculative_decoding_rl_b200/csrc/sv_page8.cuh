@@ -19,6 +19,9 @@ namespace sv {
 constexpr int PAGE8_E_MIN = -100, PAGE8_E_MAX = 119;  // bf16's largest value is below 448 * 2^120
 constexpr float PAGE8_SCALE_MIN = 7.8886090522101181e-31f;  // 2^-100
 
+// What a page's scale counts as, to every call that reads it.
+SV_DEV float page8_scale(float s) { return fmaxf(s, PAGE8_SCALE_MIN); }
+
 SV_DEV float exp2_int(int e) { return __int_as_float((e + 127) << 23); }  // 2^e for normal results
 
 // Smallest e with amax <= 448 * 2^e, clamped. 448 = 1.75 * 2^8.

@@ -2,11 +2,14 @@
 bit, the attention within bounds that follow from its documented roundings."""
 import time
 
+import numpy as np
 import pytest
 import torch
 
+import kv_reference as ref
 import speculative_decoding_rl_b200 as sv
-from test_gpu_kv_q8 import F8, gen, run_append, run_attend
+from speculative_decoding_rl_b200.session import AppendQ8Call, CommitQ8Call
+from test_gpu_kv_q8 import F8, gen, run_append, run_attend, same_bits
 
 pytestmark = pytest.mark.gpu
 
@@ -34,6 +37,38 @@ def test_append_of_long_ragged_prompts_skips_pages_among_others(how, D, Hkv):
                         positions[b, max(p * 16, start) - start + (p % 5 if p * 16 >= start else 0)] = -1 if p & 1 else 500
     run_append(True, len(lens), N, 4 if D == 128 else 5, Hkv, D, D, False, lens, seed=51, positions=pos,
                new_lens=nl, spoil=spoil, rows=500, fused=True)
+
+
+@pytest.mark.parametrize("tiny", [0.0, 2.0 ** -120])
+@pytest.mark.parametrize("D", [64, 128])
+def test_scales_below_the_smallest_count_as_it_to_append_and_commit(tiny, D):
+    # to the attention such a page's entries stand for e4m3 value * 2^-100: written back they still do
+    N, B, Hkv = 3, 3, 2
+    lens = [8, 21, 19]
+    table, nb = ref.table_for(lens, 3, np.random.default_rng(7))
+    host = list(ref.q8_pools(nb, Hkv, D, gen(57)))
+    dev = [x.cuda() for x in host]
+    host[2].fill_(2.0 ** -100)
+    dev[2].fill_(tiny)
+    rows = torch.randn((B, N, Hkv, D), generator=gen(58))
+    rows[0], rows[2] = 0, rows[2] * 2.0 ** -95           # all that is kept, and rows of its size
+    rows = rows.to(torch.bfloat16)
+    desc = sv.SvAttnDesc(B, N, Hkv, Hkv, D, 16, 3, nb)
+    ctx = torch.tensor(lens, dtype=torch.int32)
+    drows, dtable, dctx = rows.cuda(), table.cuda(), ctx.cuda()
+    append = AppendQ8Call(desc, sv.make_rope_desc(None), dev, dtable, dctx, None, drows, drows)
+    # a page that is not written keeps its scale; for the comparison it counts as the smallest
+    append.run()
+    assert ref.append(None, rows, rows, None, False, host, table, ctx, None) == append.status.tolist() == [0] * B
+    for got, want in zip(dev, host):
+        same_bits(got.clamp(min=2.0 ** -100) if got.dtype == torch.float32 else got, want)
+    dev[2].copy_(torch.where(dev[2] == 2.0 ** -100, torch.full_like(dev[2], tiny), dev[2]))
+    alen, path = torch.tensor([1, 1, 2], dtype=torch.int32), torch.tensor([[2, 0], [2, 0], [1, 2]], dtype=torch.int32)
+    commit = CommitQ8Call(desc, [dev], dtable, dctx, alen.cuda(), path.cuda())
+    new_ctx, flags = ref.commit_q8([host], table, ctx, alen, path, N)
+    assert commit.run().tolist() == new_ctx and commit.status.tolist() == flags == [0] * B
+    for got, want in zip(dev, host):
+        same_bits(got.clamp(min=2.0 ** -100) if got.dtype == torch.float32 else got, want)
 
 
 # ------------------------------------------------------------------ attention
