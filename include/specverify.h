@@ -352,8 +352,12 @@ SV_API sv_status sv_kv_append(const sv_attn_desc *desc, const sv_rope_desc *rope
  * smallest integer in [-100, 119] with max|x| <= 448 * 2^e over the page's rows
  * (finite entries; -100 for zeros), and store x * 2^-e rounded to nearest even.
  * Changing the page's power of two as rows come and go then moves its other
- * entries without another rounding (short of e4m3's subnormals), and rejected
- * drafts leave no trace: the scale only depends on the rows kept. Entries that
+ * entries without another rounding, but for those that fall among e4m3's
+ * subnormals: entries below 2^-13 of the largest the page has held, in a rejected
+ * draft too, lose bits for good. A page is looked at only when a call writes rows
+ * to it: after a commit that moves none of its rows it stays under the power of
+ * two that rejected rows asked for, until the next append to it. Entries past
+ * 448 * 2^100 come under scales that the attention does not take. Entries that
  * are not finite are stored as NaN. The attention takes any scales in
  * [2^-100, 2^100] (smaller ones, zero too, count as 2^-100), for instance from a
  * calibration; a page that a call then writes to is brought to its power of two,

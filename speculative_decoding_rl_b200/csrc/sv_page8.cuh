@@ -1,11 +1,11 @@
 // One page (16 tokens) of one KV head of the 8-bit cache, held by a warp.
 //
 // A page's entries stand for e4m3 * 2^e. e is the smallest integer in
-// [PAGE8_E_MIN, PAGE8_E_MAX] with max|x| <= 448 * 2^e over the rows kept, so a
-// page's bytes depend on its rows alone, not on what was there before. e4m3 is
-// a floating-point type: multiplying by a power of two moves no value that
-// stays in its normal range, so a page can change its scale with every row that
-// comes or goes at no loss.
+// [PAGE8_E_MIN, PAGE8_E_MAX] with max|x| <= 448 * 2^e over the rows kept whenever
+// a call writes rows to the page. e4m3 is a floating-point type: multiplying by a
+// power of two moves no value that stays in its normal range, from 2^-6 to 448, so
+// a page can change its scale with every row that comes or goes and only entries
+// below 2^-13 of the largest one lose bits.
 #pragma once
 
 #include <cuda_fp16.h>

@@ -71,6 +71,50 @@ def test_scales_below_the_smallest_count_as_it_to_append_and_commit(tiny, D):
         same_bits(got.clamp(min=2.0 ** -100) if got.dtype == torch.float32 else got, want)
 
 
+@pytest.mark.parametrize("outlier", [2.0 ** 4, 2.0 ** 10, 2.0 ** 20])
+def test_what_a_rejected_outlier_leaves_in_its_page(outlier):
+    # ten rows, a draft row far larger than they are, its rejection, an ordinary row: against the page that never held
+    # the outlier
+    D, Hkv = 128, 2
+    rows = torch.randn((1, 12, Hkv, D), generator=gen(59)).to(torch.bfloat16)
+    big = (rows[:, 11:] * outlier).to(torch.bfloat16)
+    table = torch.tensor([[0]], dtype=torch.int32).cuda()
+
+    def cache():
+        return [torch.zeros((1, Hkv, 16, D)).to(F8).cuda(), torch.zeros((1, Hkv, 16, D)).to(F8).cuda(),
+                torch.ones((1, Hkv, 2), device="cuda")]
+
+    def append(kv, ctx, x):
+        n = x.shape[1]
+        x = x.cuda()
+        AppendQ8Call(sv.SvAttnDesc(1, n, Hkv, Hkv, D, 16, 1, 1), sv.make_rope_desc(None), kv, table,
+                     torch.tensor([ctx], dtype=torch.int32).cuda(), None, x, x).run()
+        torch.cuda.synchronize()
+
+    def values(kv):
+        return (kv[0].cpu().double() * kv[2].cpu().double()[..., :1, None])[0, :, :11]
+    plain, kv = cache(), cache()
+    append(plain, 10, rows[:, :10])
+    append(plain, 11, rows[:, 10:11])
+    append(kv, 10, rows[:, :10])
+    before = kv[2].cpu().clone()
+    append(kv, 11, big)
+    raised = kv[2].cpu().clone()
+    top = big.abs().double().amax((1, 3))[0]                                   # [Hkv]
+    assert (raised > before).all() and (top <= 448 * raised[0, :, 0]).all()
+    commit = CommitQ8Call(sv.SvAttnDesc(1, 1, Hkv, Hkv, D, 16, 1, 1), [kv], table,
+                          torch.tensor([10], dtype=torch.int32).cuda(), torch.zeros(1, dtype=torch.int32).cuda(),
+                          torch.zeros((1, 1), dtype=torch.int32).cuda())
+    assert commit.run().tolist() == [10]
+    assert torch.equal(kv[2].cpu(), raised)                                    # nothing moved, nothing is written
+    append(kv, 11, rows[:, 10:11])
+    want, got, step = values(plain), values(kv), raised[0, :, :1, None].double() * 2.0 ** -9
+    kept = want.abs() >= 2.0 ** -13 * top[:, None, None]
+    assert torch.equal(got[kept], want[kept])
+    # the rest were rounded once to the subnormals of the raised scale; the last row never was under it
+    assert ((got - want).abs() <= step / 2).all() and torch.equal(got[:, 10], want[:, 10])
+
+
 # ------------------------------------------------------------------ attention
 def one_dim_scores(size, tops):
     """Scores along one dimension, whole numbers from -20 to 20 times `size`; the keys of `tops` (sequence, position)
