@@ -1,5 +1,6 @@
 """The 8-bit KV cache's calls where they are easily wrong. What append and commit leave in memory is compared bit for
 bit, the attention within bounds that follow from its documented roundings."""
+import math
 import time
 
 import numpy as np
@@ -224,3 +225,107 @@ def test_attention_wait_that_runs_out(role, limit_ms, N, Hq, D, lens):
     assert limit_ms / 1000 <= elapsed < 4.0, elapsed  # the limit, and 2 s at most for copies and products in flight
     assert torch.equal(call.run().cpu().double(), got)
     assert not call.status.any()
+
+
+# ------------------------------------------------------------------ scores that are whole numbers
+# In test_gpu_kv_q8.py a score may be off by what fp32 may lose in a sum of D products, and large scores make that
+# bound wide. Here q is a power of two in its first dimensions and zero elsewhere, and the first entries of a key add
+# up to a whole number: every score is exact but for the factor log2(e) / sqrt(D), and little is left of the bound.
+DIMS = 6
+
+
+def whole_number_keys(n):
+    """e4m3 entries [..., DIMS] whose sum is n, whole numbers of at most 2000 either way."""
+    rest, parts = n.double().clone(), []
+    for _ in range(DIMS):
+        x = rest.clamp(-448, 448)
+        unit = torch.exp2(torch.floor(torch.log2(x.abs().clamp(min=1))) - 3).clamp(min=1)
+        x = torch.trunc(x / unit) * unit
+        parts.append(x)
+        rest = rest - x
+    assert not rest.any()
+    return torch.stack(parts, -1).float().to(F8)
+
+
+def run_whole(N, Hq, D, levels, q_row, seed, mask=None, **kw):
+    """levels: for each sequence its keys' scores in powers of two (before q_row [N][Hq]'s factor), rounded to whole
+    multiples of log2(e) / sqrt(D). Compares with the formula in 64 bits."""
+    lens = [len(x) for x in levels]
+    unit = math.log2(math.e) / math.sqrt(D)
+    ns = [torch.round(torch.tensor(x, dtype=torch.float64) / unit) for x in levels]
+
+    def spoil(q, kv, table, ctx, nb):
+        q.zero_()
+        q[..., :DIMS] = q_row[None, :, :, None]
+        kv[0][:] = torch.zeros(kv[0].shape).to(F8)
+        kv[2][..., 0] = 1.0
+        for b, n in enumerate(ns):
+            keys = whole_number_keys(n)
+            for p in range(-(-len(n) // 16)):
+                part = keys[p * 16:p * 16 + 16]
+                kv[0][table[b, p], :, :len(part), :DIMS] = part
+    call, got, _, _ = run_attend(N, Hq, 2, D, lens, seed=seed, spoil=spoil, mask=mask, **kw)
+    assert not call.status.any()
+    worst = 0.0
+    for b, (C, n) in enumerate(zip(lens, ns)):
+        blk = call.block_table[b, :-(-C // 16)].long().cpu()
+        sc = call.pools[2].cpu().double()[blk][..., 1].T.repeat_interleave(16, 1)[:, :C]              # [Hkv][C]
+        v8 = call.pools[1].cpu()[blk].double().transpose(0, 1).reshape(2, -1, D)[:, :C]
+        for i in range(N):
+            seen = torch.ones(C, dtype=torch.bool)
+            for j in range(N):
+                seen[C - N + j] = j <= i if mask is None else bool(int(mask[b, i]) >> j & 1)
+            for h in range(Hq):
+                s, kvh = n * float(q_row[i, h]) * unit, h // (Hq // 2)
+                s = torch.where(seen, s, torch.full_like(s, -math.inf))
+                top = s.max()
+                w = torch.exp2(s - top)
+                w = w / w.sum()
+                o, A = w @ (v8[kvh] * sc[kvh, :, None]), w @ (v8[kvh].abs() * sc[kvh, :, None])
+                # the score's three roundings and the factor's, 2^-24 each, and that of the difference; none where
+                # all weight is on keys of one score
+                d = 0.0 if bool((w[s < top] == 0).all()) else float(s[seen].abs().max()) * 2.0 ** -21 * math.log(2)
+                bound = 2.0 ** -8 * o.abs() + (2.0 ** -9 + 2.0 ** -20 + 2 * math.expm1(d)) * A * 1.01 \
+                    + 2.0 ** -24 * float((w * sc[kvh]).max()) * (seen.double() @ v8[kvh].abs())
+                assert (bound <= 2.0 ** -6.5 * (v8[kvh].abs() * sc[kvh, :, None]).max()).all()  # it can fail
+                err = (got[b, i, h] - o).abs()
+                worst = max(worst, float((err / bound).max()))
+                assert (err <= bound).all(), (b, i, h, float((err / bound).max()))
+    return call, worst
+
+
+SHAPES = [(1, 4, 64), (5, 8, 128), (9, 10, 128), (16, 8, 64), (11, 16, 128)]
+
+
+@pytest.mark.parametrize("N,Hq,D", SHAPES)
+@pytest.mark.parametrize("step", [4.0, 7.5, 8.5, 9.0, 12.0, 20.0])
+def test_attention_maxima_that_rise_at_every_tile(N, Hq, D, step):
+    # a tile's keys lie at the last tile's largest score, one of them `step` above: whenever the running maximum is
+    # raised, the sums made before carry a good part of the answer
+    def rising(C, at):
+        x = [step * (t // 128) for t in range(C)]
+        for t in range(at, C, 128):
+            x[t] += step
+        return x
+    q_row = torch.exp2((torch.arange(N)[:, None] + torch.arange(Hq)[None]) % 3 - 1.0)
+    run_whole(N, Hq, D, [rising(1500, 77), rising(130, 3), rising(max(N, 40), 5), rising(700, 127)], q_row, seed=60)
+
+
+@pytest.mark.parametrize("N,Hq,D", SHAPES)
+def test_attention_one_maximum_over_a_split_unit(N, Hq, D):
+    # long sequences over many ranges, whose partials have maxima up to 60 powers of two apart
+    g = gen(61)
+    levels = [(torch.rand(30000, generator=g) * 4 + 56 * (torch.arange(30000) // 6000 == 3)).tolist(),
+              (torch.rand(9000, generator=g) * 6).tolist()]
+    q_row = torch.exp2((torch.arange(N)[:, None] + torch.arange(Hq)[None]) % 2 - 1.0)
+    run_whole(N, Hq, D, levels, q_row, seed=62)
+
+
+@pytest.mark.parametrize("N,Hq,D", SHAPES[1:])
+def test_attention_rows_of_far_sizes(N, Hq, D):
+    # a row's scores are its own: rows 2^80 apart in one unit, the large ones past 2^20 (one key, or equal ones, take
+    # all weight), the small ones flat
+    q_row = torch.exp2(torch.tensor([0.0, 40.0, -40.0, 1.0, 22.0])[torch.arange(N) % 5][:, None].expand(N, Hq))
+    g = gen(63)
+    levels = [(torch.rand(700, generator=g) * 8).tolist(), (torch.rand(max(N, 30), generator=g) * 8).tolist()]
+    run_whole(N, Hq, D, levels, q_row, seed=64)
