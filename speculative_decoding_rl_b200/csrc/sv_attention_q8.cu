@@ -268,13 +268,10 @@ SV_DEV uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-// The sums of a pair of products and the negated maxima, one at a time: two to an
-// instruction they would be contracted with the products.
-SV_DEV uint64_t sub_max(uint64_t x, uint64_t nm) {
-    float a, b, c, d;
-    unpack2(x, a, b);
-    unpack2(nm, c, d);
-    return pack2(__fadd_rn(a, c), __fadd_rn(b, d));
+SV_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
 }
 
 // Bounded wait on a phase, in few instructions (there are two dozen of them in
@@ -920,10 +917,10 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
                             for (int c4 = 0; c4 < CH / 4; ++c4) {
                                 const ulonglong2 q4 = reinterpret_cast<const ulonglong2 *>(qs + c0)[c4];
                                 const ulonglong2 m4 = reinterpret_cast<const ulonglong2 *>(nm + c0)[c4];
-                                // the product is rounded before the maximum, rounded alike, is taken off: the
-                                // largest score's exponent is then 0 however large it is
-                                w[2 * c4] = sub_max(mul2(mul2(pack2(x[c4 * 4], x[c4 * 4 + 1]), ksc), q4.x), m4.x);
-                                w[2 * c4 + 1] = sub_max(mul2(mul2(pack2(x[c4 * 4 + 2], x[c4 * 4 + 3]), ksc), q4.y), m4.y);
+                                // a row's scale is a power of two, so that its product is exact and the sum
+                                // with the maximum rounds the same score that the maximum was made from
+                                w[2 * c4] = fma2(mul2(pack2(x[c4 * 4], x[c4 * 4 + 1]), ksc), q4.x, m4.x);
+                                w[2 * c4 + 1] = fma2(mul2(pack2(x[c4 * 4 + 2], x[c4 * 4 + 3]), ksc), q4.y, m4.y);
                             }
 #pragma unroll
                             for (int i = 0; i < CH / 2; ++i) {
@@ -1028,7 +1025,8 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
                     // h1 stays M_NONE while nothing is visible; M_NONE - finite underflows to 0
                     const float h0 = fresh ? M_NONE : were ? -nh[ell] : -nm[ell], l0 = were ? -nm[ell] : 0.f;
                     const float h1 = fmaxf(h0, hi), l1 = fmaxf((h0 - h1) + l0, (hi - h1) + lo);
-                    nm[ell] = split ? -l1 : -h1;
+                    // a score past fp32's range: NaN for the row (the fused product would pass over it)
+                    nm[ell] = h1 == INFINITY ? NAN : split ? -l1 : -h1;
                     nh[ell] = -h1;
                     // the factor's root: V's scales may be 2^200 apart, and a row sum as large
                     as[ell] = ex2_approx(0.5f * ((h0 - h1) + (split ? l0 - l1 : 0.f)));

@@ -227,6 +227,21 @@ def test_attention_wait_that_runs_out(role, limit_ms, N, Hq, D, lens):
     assert not call.status.any()
 
 
+@pytest.mark.parametrize("N,Hq,D,lens", [(1, 4, 64, [300]), (5, 8, 128, [20000, 40]), (11, 16, 128, [700])])
+@pytest.mark.parametrize("k_scale", [2.0 ** 60, 2.0 ** 100])
+def test_attention_scores_past_fp32_are_nan_in_their_row_alone(N, Hq, D, lens, k_scale):
+    def spoil(q, kv, table, ctx, nb):
+        kv[2][..., 0] = k_scale
+        q.mul_(1 / k_scale)
+        q[0, N - 1, 1] = 2.0 ** 100       # a score of either sign beyond 2^128
+    call, got, want, tol = run_attend(N, Hq, 2, D, lens, seed=65, spoil=spoil)
+    bad = torch.zeros(got.shape[:3], dtype=torch.bool)
+    bad[0, N - 1, 1] = True
+    assert not call.status.any()
+    assert torch.equal(torch.isnan(got).all(-1), bad) and torch.equal(torch.isnan(got).any(-1), bad)
+    assert ((got - want).abs()[~bad] <= tol[~bad]).all()
+
+
 # ------------------------------------------------------------------ scores that are whole numbers
 # In test_gpu_kv_q8.py a score may be off by what fp32 may lose in a sum of D products, and large scores make that
 # bound wide. Here q is a power of two in its first dimensions and zero elsewhere, and the first entries of a key add
