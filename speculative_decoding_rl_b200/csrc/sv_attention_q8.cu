@@ -63,10 +63,12 @@ namespace {
 // rows, whose sums fill TMEM: three took 1.1 to 1.5 times as long (fewer registers
 // a thread), one left the chain of a tile exposed (64 sequences: 786 us). As many
 // columns to a warpgroup as keep its loop within 128 registers: 24 in place of 48
-// measured the same, 16 took 1.3 to 2 times as long.
+// measured the same, 16 took 1.3 to 2 times as long; 64 rows (32 sequences of 512 to
+// 16384 tokens, 8 rows of 32/4 heads) take 66 us in one warpgroup, 85 in two of 32
+// columns, whose 704 threads leave 80 registers, and 76 in two of a single range.
 template <int RP>
 struct Q8Shape {
-    static constexpr int CW = RP >= 64 ? 32 : RP;              // row columns per warpgroup
+    static constexpr int CW = RP > 64 ? 32 : RP;               // row columns per warpgroup
     static constexpr int NG = RP / CW;                         // warpgroups per range
     static constexpr int CH = CW % 16 ? 8 : 16;                // columns taken at a time
     static constexpr int NT = RP == 96 ? 1 : 2;                // ranges
