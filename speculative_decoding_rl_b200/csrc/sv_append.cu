@@ -122,9 +122,6 @@ struct Turn {
     }
 };
 
-SV_DEV float low_bf16(uint32_t w) { return __uint_as_float(w << 16); }
-SV_DEV float high_bf16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-
 // A slot's 16 entries in memory order, in fp32.
 SV_DEV void unpack_slot(const uint4 &u1, const uint4 &u2, float *y) {
     const uint32_t w[8] = {u1.x, u1.y, u1.z, u1.w, u2.x, u2.y, u2.z, u2.w};
@@ -242,10 +239,13 @@ template <bool LOOP>
 __global__ void __launch_bounds__(AP_THREADS, 4) append_kernel(const __grid_constant__ AppendParams p, int rows, int per) {
     const int b = blockIdx.y, group = AP_THREADS / rows, sub = threadIdx.x / group;
     if (p.status && blockIdx.x == 0) write_status(p, read_seq(p, b), b);
-    if (!LOOP) return rotate_row<true>(p, b, blockIdx.x * rows + sub, threadIdx.x - sub * group, group);
+    if constexpr (LOOP) {
 #pragma unroll 1
-    for (int g = 0; g < per; ++g)
-        rotate_row<true>(p, b, (blockIdx.x * per + g) * rows + sub, threadIdx.x - sub * group, group);
+        for (int g = 0; g < per; ++g)
+            rotate_row<true>(p, b, (blockIdx.x * per + g) * rows + sub, threadIdx.x - sub * group, group);
+    } else {
+        rotate_row<true>(p, b, blockIdx.x * rows + sub, threadIdx.x - sub * group, group);
+    }
 }
 
 // One page of one KV head, K or V, by two warps, each half of its rows; the

@@ -66,11 +66,12 @@ namespace {
 // measured the same, 16 took 1.3 to 2 times as long; 64 rows (32 sequences of 512 to
 // 16384 tokens, 8 rows of 32/4 heads) take 66 us in one warpgroup, 85 in two of 32
 // columns, whose 704 threads leave 80 registers, and 76 in two of a single range.
+constexpr int CH = 16;  // columns taken at a time
 template <int RP>
 struct Q8Shape {
     static constexpr int CW = RP > 64 ? 32 : RP;               // row columns per warpgroup
     static constexpr int NG = RP / CW;                         // warpgroups per range
-    static constexpr int CH = CW % 16 ? 8 : 16;                // columns taken at a time
+    static_assert(CW % CH == 0, "whole chunks of columns");
     static constexpr int NT = RP == 96 ? 1 : 2;                // ranges
     // O accumulators side by side: P's pieces enter a product's N together as far
     // as TMEM has room for their sums, the last one goes into the last sum.
@@ -206,10 +207,10 @@ SV_DEV void cut_query_row(uint8_t *a, uint8_t *b, float *scale, int lane) {
     if (lane % 16 == 0) *scale = finite ? exp2_int(e) : NAN;
 }
 
-// Sums (or maxima) of CH (8 or 16) values over the warp's lanes: the lane returns
-// that of value lane / (32 / CH). Each step halves the values a lane carries: 16
-// shuffles in place of 80 for 16 values.
-template <int CH, bool MAX = false>
+// Sums (or maxima) of CH values over the warp's lanes: the lane returns that of
+// value lane / 2. Each step halves the values a lane carries: 16 shuffles in place
+// of 80.
+template <bool MAX = false>
 SV_DEV float warp_reduce(float *v, int lane) {
     auto join = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
 #pragma unroll
@@ -221,19 +222,7 @@ SV_DEV float warp_reduce(float *v, int lane) {
             v[i] = join(keep, __shfl_xor_sync(0xffffffffu, send, bit));
         }
     }
-#pragma unroll
-    for (int bit = 16 / CH; bit > 0; bit >>= 1) v[0] = join(v[0], __shfl_xor_sync(0xffffffffu, v[0], bit));
-    return v[0];
-}
-
-// CH columns of TMEM, 8 or 16.
-template <int CH>
-SV_DEV void tmem_load(uint32_t at, float *v) {
-    if constexpr (CH == 16) tmem_ld16(at, v); else tmem_ld8(at, v);
-}
-template <int CH>
-SV_DEV void tmem_store(uint32_t at, const float *v) {
-    if constexpr (CH == 16) tmem_st16(at, v); else tmem_st8(at, v);
+    return join(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 
 // fp16 pairs of four weights -> the bytes of their first 3-bit pieces (cut off
@@ -313,7 +302,7 @@ SV_DEV bool wg_any(int id, bool v) {
 template <int D, int RP>
 __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const __grid_constant__ Q8Params P) {
     using S = Q8Shape<RP>;
-    constexpr int CW = S::CW, NG = S::NG, NT = S::NT, SB = S::SB, PB = S::PB, NQ = S::NQ, CH = S::CH;
+    constexpr int CW = S::CW, NG = S::NG, NT = S::NT, SB = S::SB, PB = S::PB, NQ = S::NQ;
     constexpr int ACC = S::ACC;
     constexpr int MATH_WARPS = S::MATH_WARPS, NTHREADS = S::THREADS;
     constexpr int WARP_LD = MATH_WARPS, WARP_MMA = MATH_WARPS + NT, WARP_AUX = MATH_WARPS + 2 * NT;
@@ -731,10 +720,10 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
 #pragma unroll 1
             for (int c0 = 0; c0 < CW; c0 += CH) {
                 float l[CH];
-                tmem_load<CH>(tm_l + c0, l);
+                tmem_ld16(tm_l + c0, l);
                 tmem_wait_ld();
-                const float v = warp_reduce<CH>(l, lane);
-                if (lane % (32 / CH) == 0) red[wiw * RP + c0 + lane / (32 / CH)] = v;
+                const float v = warp_reduce<>(l, lane);
+                if (lane % 2 == 0) red[wiw * RP + c0 + lane / 2] = v;
             }
             wg_sync(1 + wg);
             const int fh = uhr / p.RC, frc = uhr - fh * p.RC;
@@ -764,11 +753,11 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
 #pragma unroll 1
             for (int c0 = 0; c0 < CW; c0 += CH) {
                 float o[CH];
-                tmem_load<CH>(tm_o + c0, o);
+                tmem_ld16(tm_o + c0, o);
 #pragma unroll
                 for (int i = 1; i < ACC; ++i) {
                     float o1[CH];
-                    tmem_load<CH>(tm_o + i * RP + c0, o1);
+                    tmem_ld16(tm_o + i * RP + c0, o1);
                     tmem_wait_ld();
 #pragma unroll
                     for (int c = 0; c < CH; ++c) o[c] += o1[c];
@@ -872,7 +861,7 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
 #pragma unroll 1
                 for (int c0 = 0; c0 < CW; c0 += CH) {
                     float x[CH];
-                    tmem_load<CH>(saddr + c0, x);
+                    tmem_ld16(saddr + c0, x);
                     tmem_wait_ld();
 #pragma unroll
                     for (int c = 0; c < CH; ++c) {
@@ -881,7 +870,7 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
                         const bool bit = p.mask ? (umask[i] >> (newk & 63) & 1ull) != 0 : newk <= i;
                         if (newk >= 0 && !(bit && key < uC)) x[c] = -INFINITY;
                     }
-                    tmem_store<CH>(saddr + c0, x);
+                    tmem_st16(saddr + c0, x);
                 }
                 tmem_wait_st();
             }
@@ -895,7 +884,7 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
             // is done again, its weights taken out of the row sums first.
             const int pb = lt % PB;
             uint8_t *pdst = p_buf + pb * L.p_bytes + ell * 16;
-            auto p_at = [&](int c0) { return (col0 + c0) / 16 * GROUP + (col0 + c0) % 16; };
+            auto p_at = [&](int c0) { return (col0 + c0) / 16 * GROUP; };
             if (lt >= PB && ok) ok = wait_w(&o_full[pb], ((lt - PB) / PB) & 1);  // P is free
             const bool fresh = first;  // a unit in two parts raises at every tile, before its weights are made
             bool raise = first || split, leave = false;
@@ -909,9 +898,9 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
 #pragma unroll 1
                         for (int c0 = 0; c0 < CW; c0 += CH) {
                             float x[CH], l[CH];
-                            tmem_load<CH>(saddr + c0, x);
+                            tmem_ld16(saddr + c0, x);
                             tmem_wait_ld();
-                            tmem_load<CH>(tm_l + c0, l);
+                            tmem_ld16(tm_l + c0, l);
                             // in phases over the chunk, so that no value waits for the one before
                             uint64_t w[CH / 2];
                             uint32_t h[CH / 2], piece[3][CH / 4];
@@ -953,15 +942,11 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
                             for (int j = 0; j < 3; ++j)
 #pragma unroll
                                 for (int c4 = 0; c4 < CH / 4; ++c4) piece[j][c4] = cut_piece(h + 2 * c4, j == 2);
-                            tmem_store<CH>(tm_l + c0, l);
+                            tmem_st16(tm_l + c0, l);
 #pragma unroll
                             for (int j = 0; j < 3; ++j)
-                                if constexpr (CH == 16)
-                                    *reinterpret_cast<uint4 *>(pdst + (j * (RP / 16) * GROUP + p_at(c0))) =
-                                        make_uint4(piece[j][0], piece[j][1], piece[j][2], piece[j][3]);
-                                else
-                                    *reinterpret_cast<uint2 *>(pdst + (j * (RP / 16) * GROUP + p_at(c0))) =
-                                        make_uint2(piece[j][0], piece[j][1]);
+                                *reinterpret_cast<uint4 *>(pdst + (j * (RP / 16) * GROUP + p_at(c0))) =
+                                    make_uint4(piece[j][0], piece[j][1], piece[j][2], piece[j][3]);
                         }
                         tmem_wait_st();
                     }
@@ -974,8 +959,8 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
 #pragma unroll 1
                 for (int c0 = 0; c0 < CW; c0 += CH) {
                     float y[CH], l[CH];
-                    tmem_load<CH>(saddr + c0, y);
-                    if (!fresh) tmem_load<CH>(tm_l + c0, l);
+                    tmem_ld16(saddr + c0, y);
+                    if (!fresh) tmem_ld16(tm_l + c0, l);
                     tmem_wait_ld();
 #pragma unroll
                     for (int c = 0; c < CH; ++c) {
@@ -986,10 +971,10 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
                                                          : l[c];
                         y[c] = __fadd_rn(e, lv);
                     }
-                    tmem_store<CH>(tm_l + c0, l);
-                    const float m = warp_reduce<CH, true>(y, lane);
+                    tmem_st16(tm_l + c0, l);
+                    const float m = warp_reduce<true>(y, lane);
                     big |= fabsf(m) >= TWO_PARTS_FROM && fabsf(m) < INFINITY;
-                    if (lane % (32 / CH) == 0) red[wiw * RP + c0 + lane / (32 / CH)] = m;
+                    if (lane % 2 == 0) red[wiw * RP + c0 + lane / 2] = m;
                 }
                 tmem_wait_st();
                 auto tile_max = [&]() {  // of column ell
@@ -1006,15 +991,15 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
 #pragma unroll 1
                         for (int c0 = 0; c0 < CW; c0 += CH) {
                             float y[CH];
-                            tmem_load<CH>(saddr + c0, y);
+                            tmem_ld16(saddr + c0, y);
                             tmem_wait_ld();
 #pragma unroll
                             for (int c = 0; c < CH; ++c) {
                                 const float e = __fmul_rn(y[c] * ks1, qs[c0 + c]);
                                 y[c] = part ? __fadd_rn(__fsub_rn(e, as[c0 + c]), lv) : e;
                             }
-                            const float m = warp_reduce<CH, true>(y, lane);
-                            if (lane % (32 / CH) == 0) red[wiw * RP + c0 + lane / (32 / CH)] = m;
+                            const float m = warp_reduce<true>(y, lane);
+                            if (lane % 2 == 0) red[wiw * RP + c0 + lane / 2] = m;
                         }
                         wg_sync(1 + wg);
                         if (ell < CW) (part ? lo : hi) = tile_max();
@@ -1044,11 +1029,11 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
                             const int c0 = i / (ACC + 1) * CH, k = i % (ACC + 1);
                             const uint32_t at = k == ACC ? tm_l + c0 : tm_o + k * RP + c0;
                             float o[CH];
-                            tmem_load<CH>(at, o);
+                            tmem_ld16(at, o);
                             tmem_wait_ld();
 #pragma unroll
                             for (int c = 0; c < CH; ++c) o[c] = o[c] * as[c0 + c] * as[c0 + c];
-                            tmem_store<CH>(at, o);
+                            tmem_st16(at, o);
                         }
                         tmem_wait_st();
                     }
@@ -1059,14 +1044,14 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
 #pragma unroll 1
                     for (int c0 = 0; c0 < CW; c0 += CH) {
                         float y[CH];
-                        tmem_load<CH>(saddr + c0, y);
+                        tmem_ld16(saddr + c0, y);
                         tmem_wait_ld();
 #pragma unroll
                         for (int c = 0; c < CH; ++c) {
                             const float e = __fmul_rn(y[c] * ks1, qs[c0 + c]);
                             y[c] = __fadd_rn(e, nh[c0 + c]) * __int_as_float(0x7F000000 - __float_as_int(qs[c0 + c]));
                         }
-                        tmem_store<CH>(saddr + c0, y);
+                        tmem_st16(saddr + c0, y);
                     }
                     tmem_wait_st();
                     ksc = pack2(1.f, 1.f);

@@ -100,10 +100,10 @@ __global__ void __launch_bounds__(32 * CQ_WARPS, 3) kv_commit_q8_kernel(const __
             const size_t at = (size_t)dst * P.Hkv + h;
             __syncwarp();  // every lane has read the page before one writes it
             auto get = [&](int st, int i, float &x, float &y) { unpack_e4m3(raw[st], i, scale[st], x, y); };
-            const int e = page8_exponent(warp_max(Page8<D>::template top<Page8<D>::STEPS>(0, kept, lane, get)));
+            const int e = page8_exponent(warp_max(Page8<D>::top(kept, lane, get)));
             if (lane == 0) layer.scales[2 * at + is_v] = exp2_int(e);
-            Page8<D>::template write<Page8<D>::STEPS>(pool + at * PAGE * D, e, 0, kept, lane, get,
-                                                            [&](int st) { return stays >> st & 1 && scale[st] == exp2_int(e); });
+            Page8<D>::write(pool + at * PAGE * D, e, kept, lane, get,
+                            [&](int st) { return stays >> st & 1 && scale[st] == exp2_int(e); });
         }
         __syncwarp();
     }

@@ -64,15 +64,15 @@ struct Page8 {
     SV_DEV static int row(int step, int lane) { return step * ROWS_STEP + lane / LANES_ROW; }
     SV_DEV static int col(int lane) { return lane % LANES_ROW * 8; }
 
-    // Steps [S0, S0 + NS) of a page's rows [0, kept). get(step, i, a, b) gives
+    // A page's rows [0, kept). get(step, i, a, b) gives
     // entries 2i and 2i + 1 of the lane's 8 of a step in fp32.
     // Largest magnitude of the lane's entries:
-    template <int NS, typename Get>
-    SV_DEV static float top(int S0, int kept, int lane, Get get) {
+    template <typename Get>
+    SV_DEV static float top(int kept, int lane, Get get) {
         float amax = 0.f;
 #pragma unroll
-        for (int s = 0; s < NS; ++s)
-            if (row(S0 + s, lane) < kept)
+        for (int s = 0; s < STEPS; ++s)
+            if (row(s, lane) < kept)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     float a, b;
@@ -83,12 +83,12 @@ struct Page8 {
     }
     // The rows under 2^e, to `page` (16 x D bytes), but for those that are(step)
     // says are there already; rows past `kept` stay as they were.
-    template <int NS, typename Get, typename Are>
-    SV_DEV static void write(uint8_t *page, int e, int S0, int kept, int lane, Get get, Are are) {
+    template <typename Get, typename Are>
+    SV_DEV static void write(uint8_t *page, int e, int kept, int lane, Get get, Are are) {
         const float inv = exp2_int(-e);
 #pragma unroll
-        for (int s = 0; s < NS; ++s) {
-            const int r = row(S0 + s, lane);
+        for (int s = 0; s < STEPS; ++s) {
+            const int r = row(s, lane);
             if (r >= kept || are(s)) continue;
             uint32_t w[4];
 #pragma unroll
