@@ -115,7 +115,9 @@ cudaError_t launch_kv_commit_q8(const CommitQ8Launch &c, cudaStream_t stream) {
     // A warp takes every stride-th job of its sequence: one each while the warps
     // fit the SMs (24 a piece at this kernel's 80 registers), more beyond (64 paths
     // in 48 layers: 35 us in place of 72 with a CTA of its own for each job).
-    const long long jobs = 2LL * c.Hkv * c.L, fit = 148LL * 24;
+    const int sms = attention_num_ctas();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    const long long jobs = 2LL * c.Hkv * c.L, fit = 24LL * sms;
     const long long per = (jobs * c.B + fit - 1) / fit;
     const long long warps = (jobs + per - 1) / per;
     const unsigned ctas = (unsigned)((warps + CQ_WARPS - 1) / CQ_WARPS);
