@@ -381,8 +381,9 @@ SV_API sv_status sv_kv_append_q8(const sv_attn_desc *desc, const sv_rope_desc *r
  * flags (q and out bf16; the pools 16-byte aligned, scales 8-byte aligned; out,
  * workspace and status_flags must not overlap an input or one another).
  * A page with a block id outside the pool reads as zeros. Scores and sums are
- * fp32 (a score past its range gives NaN for the row); q is used to 2^-17 of its row's largest entry, a key's weight to 2^-9 of
- * itself and, far below the row's largest, to 2^-24 of that. A NaN entry of K
+ * fp32 (a score past its range gives NaN for the row); q is used to 2^-17 of its
+ * row's largest entry, or to 2^-129, a key's weight to 2^-9 of itself and, far
+ * below the row's largest, to 2^-24 of that. A NaN entry of K
  * makes NaN of the rows that see its key, of V that entry of theirs; a row of q
  * with an entry that is not finite gives NaN. Rows that do not see a key are not
  * touched by what it holds. */

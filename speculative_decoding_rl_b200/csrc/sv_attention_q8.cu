@@ -189,9 +189,11 @@ SV_DEV void cut_query_row(uint8_t *a, uint8_t *b, float *scale, int lane) {
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     const bool finite = top < 0x7F800000u;
-    // |x| <= 448 * 2^e. e stays where 2^-e and 2^e are normal.
+    // |x| <= 448 * 2^e, e no smaller than -119: a unit in two parts divides differences
+    // of scores, up to 2^7 for a row this small, by 2^e. The smallest rows are then held
+    // to 2^-129, which moves a score by 2^-16 at most (448 * 2^100 the largest key entry).
     const int ex = (int)(top >> 23) - 127;
-    const int e = max(-126, (top & 0x7FFFFFu) <= 0x600000u ? ex - 8 : ex - 7);
+    const int e = max(-119, (top & 0x7FFFFFu) <= 0x600000u ? ex - 8 : ex - 7);
     const float inv = finite ? exp2_int(-e) : 0.f;
     uint32_t hi[E / 4] = {}, lo[E / 4] = {};
 #pragma unroll

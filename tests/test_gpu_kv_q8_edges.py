@@ -344,3 +344,15 @@ def test_attention_rows_of_far_sizes(N, Hq, D):
     g = gen(63)
     levels = [(torch.rand(700, generator=g) * 8).tolist(), (torch.rand(max(N, 30), generator=g) * 8).tolist()]
     run_whole(N, Hq, D, levels, q_row, seed=64)
+
+
+@pytest.mark.parametrize("N,Hq,D", SHAPES[1:])
+@pytest.mark.parametrize("small", [2.0 ** -126, 2.0 ** -110, 2.0 ** -60, 1.0, 2.0 ** 10])
+def test_attention_rows_beside_one_whose_scores_grow_past_2_20(N, Hq, D, small):
+    # the first tile's scores are all 0, then one row's are huge: what the others have summed up under V's scales
+    # of 2^4 to 2^8 stays
+    q_row = torch.full((N, Hq), small)
+    q_row[N // 2, 1] = 2.0 ** 30
+    g = gen(66)
+    levels = [[0.0] * 130 + (torch.rand(570, generator=g) * 8).tolist(), (torch.rand(max(N, 30), generator=g)).tolist()]
+    run_whole(N, Hq, D, levels, q_row, seed=67, lo=4, hi=9)
