@@ -829,17 +829,16 @@ __global__ void __launch_bounds__(32 * COMBINE_ROWS, MIN_CTAS) attn_combine_kern
     float M = mk;
     for (int k = lane + 32; k < n; k += 32) M = fmaxf(M, __ldcg(seg0 + (size_t)k * sf + (size_t)RU * D + r));
     M = warp_max(M);
-    // The 8-bit cache's maxima hold V's scale, which may be 2^200 apart, and the
-    // sums the inverse of it: the factor comes to them in two halves.
-    constexpr float HALF = UC == UNIT_COST_Q8 ? 0.5f : 1.f;
-    auto scaled = [](float w, float l) { return HALF == 1.f ? w * l : w * l * w; };
-    const float wh = lane < n ? exp2f((mk - M) * HALF) : 0.f;  // an empty segment holds l = 0
-    const float wl = HALF == 1.f ? wh : wh * wh;
-    float L = scaled(wh, lk);
+    // The 8-bit cache's maxima may hold V's scale or leave it to the sums, whose sizes
+    // differ by up to 2^200 then: the factor comes to them in two halves.
+    constexpr bool HALVES = UC == UNIT_COST_Q8;
+    auto factor = [&](float m) { return exp2f(HALVES ? (m - M) * 0.5f : m - M); };
+    auto add = [](float w, float x, float sum) { return fmaf(w, HALVES ? w * x : x, sum); };
+    const float wl = lane < n ? factor(mk) : 0.f;  // an empty segment holds l = 0
+    float L = add(wl, lk, 0.f);
     for (int k = lane + 32; k < n; k += 32) {
         const float *sg = seg0 + (size_t)k * sf + (size_t)RU * D;
-        const float w = exp2f((__ldcg(sg + r) - M) * HALF), l = __ldcg(sg + RU + r);
-        L = HALF == 1.f ? fmaf(w, l, L) : L + scaled(w, l);
+        L = add(factor(__ldcg(sg + r)), __ldcg(sg + RU + r), L);
     }
     L = warp_sum(L);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -847,8 +846,8 @@ __global__ void __launch_bounds__(32 * COMBINE_ROWS, MIN_CTAS) attn_combine_kern
     for (int k = 0; k < COMBINE_REG_SEGS; ++k) {
         const float w = __shfl_sync(0xffffffffu, wl, k);
         if (k < n) {
-            acc.x = fmaf(w, ov[k].x, acc.x); acc.y = fmaf(w, ov[k].y, acc.y);
-            acc.z = fmaf(w, ov[k].z, acc.z); acc.w = fmaf(w, ov[k].w, acc.w);
+            acc.x = add(w, ov[k].x, acc.x); acc.y = add(w, ov[k].y, acc.y);
+            acc.z = add(w, ov[k].z, acc.z); acc.w = add(w, ov[k].w, acc.w);
         }
     }
     // the rest (a unit split over many CTAs, at small B) four at a time, the
@@ -865,9 +864,9 @@ __global__ void __launch_bounds__(32 * COMBINE_ROWS, MIN_CTAS) attn_combine_kern
         for (int j = 0; j < 4; ++j) {
             const int k = k0 + j;  // partials past n were loaded as zeros
             const float w = k < 32 ? __shfl_sync(0xffffffffu, wl, k & 31)
-                                   : (k < n ? exp2f(__ldcg(seg0 + (size_t)k * sf + (size_t)RU * D + r) - M) : 0.f);
-            acc.x = fmaf(w, ob[j].x, acc.x); acc.y = fmaf(w, ob[j].y, acc.y);
-            acc.z = fmaf(w, ob[j].z, acc.z); acc.w = fmaf(w, ob[j].w, acc.w);
+                                   : (k < n ? factor(__ldcg(seg0 + (size_t)k * sf + (size_t)RU * D + r)) : 0.f);
+            acc.x = add(w, ob[j].x, acc.x); acc.y = add(w, ob[j].y, acc.y);
+            acc.z = add(w, ob[j].z, acc.z); acc.w = add(w, ob[j].w, acc.w);
         }
     }
     if (!dl) return;

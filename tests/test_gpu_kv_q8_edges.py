@@ -262,7 +262,7 @@ def whole_number_keys(n):
     return torch.stack(parts, -1).float().to(F8)
 
 
-def run_whole(N, Hq, D, levels, q_row, seed, mask=None, **kw):
+def run_whole(N, Hq, D, levels, q_row, seed, mask=None, scales=None, **kw):
     """levels: for each sequence its keys' scores in powers of two (before q_row [N][Hq]'s factor), rounded to whole
     multiples of log2(e) / sqrt(D). Compares with the formula in 64 bits."""
     lens = [len(x) for x in levels]
@@ -279,6 +279,8 @@ def run_whole(N, Hq, D, levels, q_row, seed, mask=None, **kw):
             for p in range(-(-len(n) // 16)):
                 part = keys[p * 16:p * 16 + 16]
                 kv[0][table[b, p], :, :len(part), :DIMS] = part
+        if scales:
+            scales(kv, table)
     call, got, _, _ = run_attend(N, Hq, 2, D, lens, seed=seed, spoil=spoil, mask=mask, **kw)
     assert not call.status.any()
     worst = 0.0
@@ -356,3 +358,21 @@ def test_attention_rows_beside_one_whose_scores_grow_past_2_20(N, Hq, D, small):
     g = gen(66)
     levels = [[0.0] * 130 + (torch.rand(570, generator=g) * 8).tolist(), (torch.rand(max(N, 30), generator=g)).tolist()]
     run_whole(N, Hq, D, levels, q_row, seed=67, lo=4, hi=9)
+
+
+@pytest.mark.parametrize("N,Hq,D", SHAPES[1:])
+def test_attention_of_a_split_unit_in_two_parts_under_far_scales(N, Hq, D):
+    # one row's scores pass 2^20, so that the unit's partials carry V's scales in their sums; of another row the largest
+    # key, 2^200 above the rest, has V's smallest scale, and keys of the largest scale count as much
+    C = 6000
+    q_row = torch.ones((N, Hq))
+    q_row[N // 2, 1] = 2.0 ** 25
+    x = torch.rand(C, generator=gen(68)) * 6
+    x[443] = 200
+
+    def scales(kv, table):
+        kv[2][..., 1] = 2.0 ** -100
+        for p in range(C // 16):
+            if p % 7 == 3 and p != 443 // 16:
+                kv[2][table[0, p], :, 1] = 2.0 ** 99
+    run_whole(N, Hq, D, [x.tolist()], q_row, seed=69, scales=scales)
