@@ -638,15 +638,9 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
             idv = ids;
             hv = h;
         }
-        // Copies that nobody waited for, because someone gave up, land before the CTA can
-        // exit. Once the range's products are through, all were waited for.
-        if (lane == 0 && !(wait_phase(done_bar, 0, abort_flag, P.wait_ns) && !*abort_flag)) {
-#pragma unroll 1
-            for (int i = max(0, issued[0] - NK); i < issued[0]; ++i)
-                mbar_wait_time(&k_full[i % NK], (i / NK) & 1, WAIT_LIMIT_NS);
-#pragma unroll 1
-            for (int i = max(0, issued[1] - NV); i < issued[1]; ++i)
-                mbar_wait_time(&v_full[i % NV], (i / NV) & 1, WAIT_LIMIT_NS);
+        if (lane == 0) {  // for the teardown
+            scratch[8 * r + 5] = issued[0];
+            scratch[8 * r + 6] = issued[1];
         }
     } else {
         // ------------------------------ softmax ------------------------------
@@ -893,8 +887,7 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
             // a second raise in a row cannot come: the maxima are the tile's own then
 #pragma unroll 1
             for (int tries = 0;; ++tries) {
-                const bool counted = !raise;  // this tile's weights are in the row sums
-                if (counted) {
+                if (!raise) {
                     __half2 top2 = __float2half2_rn(0.f);
                     if (ok) {
 #pragma unroll 1
@@ -956,10 +949,12 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
                     if (!raise) break;
                 }
                 if ((leave = wg_any(1 + wg, !ok))) break;
-                // tile column maxima over the 128 keys; this tile's weights out of the row sums
-                bool big = false;
+                // tile column maxima over the 128 keys; this tile's weights out of the row sums (the
+                // weights of a unit in two parts are made after this)
+                const bool were = split && !fresh;
+                bool big = were;
 #pragma unroll 1
-                for (int c0 = 0; c0 < CW; c0 += CH) {
+                for (int c0 = 0; c0 < CW && !were; c0 += CH) {
                     float y[CH], l[CH];
                     tmem_ld16(saddr + c0, y);
                     if (!fresh) tmem_ld16(tm_l + c0, l);
@@ -968,9 +963,7 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
                     for (int c = 0; c < CH; ++c) {
                         const float e = __fmul_rn(y[c] * ks1, qs[c0 + c]);
                         // a sum that overflowed held nothing that counts beside the weight that made it so
-                        l[c] = fresh || l[c] == INFINITY ? 0.f
-                               : counted                 ? l[c] - ex2_approx(__fadd_rn(e, nm[c0 + c]))
-                                                         : l[c];
+                        l[c] = fresh || l[c] == INFINITY ? 0.f : l[c] - ex2_approx(__fadd_rn(e, nm[c0 + c]));
                         y[c] = __fadd_rn(e, lv);
                     }
                     tmem_st16(tm_l + c0, l);
@@ -983,8 +976,7 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
                     return fmaxf(fmaxf(red[ell], red[RP + ell]), fmaxf(red[2 * RP + ell], red[3 * RP + ell]));
                 };
                 // once a unit's maxima have two parts, all its tiles' have
-                const bool were = split && !fresh;
-                split = wg_any(1 + wg, big || were);
+                split = wg_any(1 + wg, big);
                 float hi = 0.f, lo = 0.f;
                 if (ell < CW && !split) hi = tile_max();
                 if (__builtin_expect(split, 0)) {  // hi: the largest score; lo: what the scales add to it
@@ -1081,6 +1073,14 @@ __global__ void __launch_bounds__(Q8Shape<RP>::THREADS, 1) attn_q8_kernel(const 
     // ----------------------------- teardown -------------------------------
     tc_fence_before();
     __syncthreads();
+    if (*abort_flag && tid < NT * (NK + NV)) {
+        // someone gave up: copies that nobody waited for land before the CTA exits. One
+        // thread to a slot of K and V of each range.
+        const int rr = tid / (NK + NV), at = tid % (NK + NV), ring = at < NK ? NK : NV, slot = at < NK ? at : at - NK;
+        const int uses = (scratch[8 * rr + (at < NK ? 5 : 6)] - slot + ring - 1) / ring;
+        uint64_t *full = reinterpret_cast<uint64_t *>(base + L.off_bar) + rr * nrb + (at < NK ? slot : 2 * NK + slot);
+        if (uses > 0) mbar_wait_time(full, (uses - 1) & 1, WAIT_LIMIT_NS);
+    }
     if (*abort_flag && p.status)
         for (int b = tid; b < p.B; b += NTHREADS) atomicOr(p.status + b, SV_FLAG_TIMEOUT);
     if (warp == WARP_MMA) {
