@@ -40,10 +40,11 @@
 //                zeroed before a tile goes to its product; the pages' scales.
 //
 // Measured at D = 128: 64 sequences of 512 to 32768 tokens, 45 rows a unit (1.05
-// GB) 262 us in short runs (4.0 TB/s; the loads alone would take 160 us), of which
+// GB) 255 us in short runs (4.1 TB/s; the loads alone would take 160 us), of which
 // a range's tile takes 1.9 us and a unit's start and end 7 us; 16 trees of 88 rows
-// over 24576 tokens (0.41 GB) 184 us. What bounds it is the softmax's instruction
-// stream, 3550 warp instructions a tile, not memory (50 %) or the tensor unit (43 %).
+// over 24576 tokens (0.41 GB) 173 us; 294 and 183 us one after the other under the
+// power cap. What bounds it is the softmax's chain of 3580 warp instructions a tile,
+// two tiles in flight: no unit is full (issue 49 %, memory 50 %, tensor unit 49 %).
 #include <string.h>
 
 #include <type_traits>
