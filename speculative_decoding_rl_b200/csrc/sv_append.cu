@@ -378,11 +378,22 @@ cudaError_t launch_append(const AppendParams &params, bool q8, cudaStream_t stre
     p.slots = p.R / 16 + ((p.D - p.R) / 8 + 1) / 2;
     const int rows = rows_per_cta(p, !q8);
     const long long groups = (p.N + rows - 1) / rows, pages = (p.N + PAGE - 2) / PAGE + 1;  // that N positions can touch
-    // Ragged prompts leave CTAs without rows, which still wait for their length:
-    // with many rows to a sequence a CTA goes on to the next ones (16 prompts of up
-    // to 1500 rows into the 8-bit cache: 75 us with one group to a CTA, 67 with four,
-    // 68 with eight).
-    const int per = p.new_lens && p.N >= 256 ? 4 : 1;
+    const int kv_parts = q8 ? (2 * p.Hkv + AP_WARPS / 2 - 1) / (AP_WARPS / 2) : 0;
+    const bool q_rows = !q8 || p.q;
+    // Groups of rows, or pages, to a CTA. Many short CTAs, of which the shorter prompts of
+    // a ragged batch leave some without rows, are worth taking four at a time once they
+    // are seven to nine waves; with fewer, SMs run out of them. One group against four,
+    // 32 + 16 heads of 128, rows of equal length (ragged) into the 8-bit cache: 16 x
+    // 1500 123 against 113 us (76 against 68), 16 x 600 54 against 49 (35 against 31), 2 x
+    // 2000 24.5 and 24.5 (22.2 and 22.4), 1 x 2000 12.9 against 14, 1 x 256 4.5 against
+    // 9.6; bf16: 64 x 300 92 against 90 (63 against 56), 2 x 2000 23 against 24, 1 x
+    // 256 3.5 against 6.9. Eight measured as four.
+    int per = 1;
+    if (p.N >= 256) {
+        const int sms = attention_num_ctas();
+        if (sms <= 0) return cudaErrorInvalidDevice;
+        if (p.B * (pages * kv_parts + (q_rows ? groups : 0)) >= 28LL * sms) per = 4;
+    }
     const long long row_ctas = (groups + per - 1) / per;
     if (!q8) {
         const dim3 grid((unsigned)row_ctas, (unsigned)p.B);
@@ -392,10 +403,9 @@ cudaError_t launch_append(const AppendParams &params, bool q8, cudaStream_t stre
             append_kernel<false><<<grid, AP_THREADS, 0, stream>>>(p, rows, per);
         return cudaGetLastError();
     }
-    const int kv_parts = (2 * p.Hkv + AP_WARPS / 2 - 1) / (AP_WARPS / 2);
     const long long kv_ctas = (pages + per - 1) / per * kv_parts;
     if (kv_ctas + row_ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    const dim3 grid((unsigned)(kv_ctas + (p.q ? row_ctas : 0)), (unsigned)p.B);
+    const dim3 grid((unsigned)(kv_ctas + (q_rows ? row_ctas : 0)), (unsigned)p.B);
     if (p.D == 128)
         append_q8_kernel<128><<<grid, AP_THREADS, 0, stream>>>(p, (int)kv_ctas, kv_parts, rows, per);
     else
